@@ -461,3 +461,318 @@ def alloc_recv(shape: Shape, device, fill: Optional[int] = None):
 def alloc_workspace(shape: Shape, device) -> Optional[torch.Tensor]:
     n = moe_dispatch_workspace_size(shape)
     return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------------------
+# include/moe_experts.h: the experts' matrix product, the balance loss and the
+# gradients.  These calls run on the device of their tensors, which must all be
+# on one; without a stream they use that device's current one.
+# ---------------------------------------------------------------------------
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = 0, 1, 2, 3
+
+
+class _Linear(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
+
+
+_f32, _size = ctypes.c_float, ctypes.c_size_t
+_shape_p, _layout_p, _linear_p = (ctypes.POINTER(c) for c in (_Shape, _Layout, _Linear))
+_lib.moe_expert_matmul.argtypes = [_shape_p, _linear_p, _vp, _vp, _layout_p, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _vp]
+_lib.moe_expert_matmul.restype = _i32
+_lib.moe_expert_matmul_backward_workspace_size.argtypes = [_shape_p, _linear_p]
+_lib.moe_expert_matmul_backward_workspace_size.restype = _size
+_lib.moe_expert_matmul_backward.argtypes = [_shape_p, _linear_p, _vp, _vp, _layout_p, _vp, _vp,
+                                            _vp, _vp, _vp, _vp, _size, _vp]
+_lib.moe_expert_matmul_backward.restype = _i32
+_lib.moe_combine_backward.argtypes = [_shape_p, _vp, _vp, _layout_p, _vp, _vp, _vp, _vp]
+_lib.moe_combine_backward.restype = _i32
+_lib.moe_balance_loss_workspace_size.argtypes = [_i32, _i32, _i32]
+_lib.moe_balance_loss_workspace_size.restype = _size
+_lib.moe_balance_loss.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _f32, _vp,
+                                  _vp, _vp, _vp, _vp, _size, _vp]
+_lib.moe_balance_loss.restype = _i32
+_lib.moe_route_backward_workspace_size.argtypes = [_i32, _i32]
+_lib.moe_route_backward_workspace_size.restype = _size
+_lib.moe_route_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32,
+                                    _f32, _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]
+_lib.moe_route_backward.restype = _i32
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)          # values, or their bits
+_E4M3 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
+_BYTES = (torch.uint8, torch.int8)
+
+
+@dataclasses.dataclass(frozen=True)
+class Linear:
+    """One linear layer of every expert (mirrors moe_linear)."""
+    in_features: int
+    out_features: int
+    activation: int = MOE_ACT_NONE
+
+    def c(self) -> _Linear:
+        return _Linear(self.in_features, self.out_features, self.activation)
+
+    @property
+    def pre_features(self) -> int:
+        """Columns before the activation (weight rows per expert)."""
+        return self.out_features * (2 if self.activation == MOE_ACT_SWIGLU else 1)
+
+
+def _all(call: str, specs) -> int:
+    """Check (name, tensor, dtypes, elements, required) entries; returns the
+    one device index all tensors are on."""
+    dev = -1
+    for name, t, dtypes, numel, required in specs:
+        if t is None:
+            if required and numel > 0:
+                raise ValueError(f"{call}: {name} is required")
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{call}: {name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{call}: {name} must be a GPU tensor (got {t.device})")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{call}: {name} must be {dtypes[0]} (got {t.dtype})")
+        if not t.is_contiguous():
+            raise ValueError(f"{call}: {name} must be contiguous")
+        if t.numel() < numel:
+            raise ValueError(f"{call}: {name} holds {t.numel()} elements, {numel} are needed")
+        d = t.get_device()
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{call}: {name} is on cuda:{d}, other tensors on cuda:{dev}")
+    return dev
+
+
+def _run(call: str, dev: int, stream, fn, *args) -> None:
+    if dev < 0 or dev == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream) if dev >= 0 else None), call)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), call)
+
+
+def _workspace(nbytes: int, given, dev: int, stream, call: str):
+    """The caller's workspace, or one of the call's own (kept from reuse until
+    the stream has passed it)."""
+    if given is not None or nbytes == 0:
+        return given
+    if dev < 0:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(_stream(stream), device=torch.device("cuda", dev))
+        ws.record_stream(s)
+    return ws
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _segments(shape: Shape, layout: Optional[Layout]):
+    if layout is None:
+        return ()
+    return (("layout.expert_counts", layout.expert_counts, _I32, shape.num_experts, True),
+            ("layout.expert_offsets", layout.expert_offsets, _I32, shape.num_experts, True))
+
+
+def _maybe(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def moe_expert_matmul(shape: Shape, linear: Linear, x: torch.Tensor,
+                      x_scales: Optional[torch.Tensor], layout: Optional[Layout],
+                      weight: torch.Tensor, weight_scales: Optional[torch.Tensor],
+                      bias: Optional[torch.Tensor], residual: Optional[torch.Tensor],
+                      y: torch.Tensor, pre: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y = act(x weight[e]^T + bias[e]) + residual on every expert's placed rows.
+
+    layout None: a dense product over num_tokens rows (num_experts == top_k == 1)."""
+    c, dev = "moe_expert_matmul", -1
+    rows = _rows(shape)
+    if rows is not None:
+        E, K, F, P = shape.num_experts, linear.in_features, linear.out_features, linear.pre_features
+        rows = rows if layout is not None else shape.num_tokens
+        fp8 = shape.fp8
+        rt = _E4M3 if fp8 else _BF16
+        dev = _all(c, (("x", x, rt, rows * K, True),
+                       ("x_scales", x_scales, _F32, rows * (K // 128) if fp8 else 0, fp8),
+                       ("weight", weight, rt, E * P * K, True),
+                       ("weight_scales", weight_scales, _F32,
+                        E * (P // 128) * (K // 128) if fp8 else 0, fp8),
+                       ("bias", bias, _F32, E * P, False),
+                       ("residual", residual, _BF16, rows * F, False),
+                       ("y", y, _BF16, rows * F, True), ("pre", pre, _BF16, rows * P, False),
+                       *_segments(shape, layout)))
+    lay = None if layout is None else layout.c()
+    _run(c, dev, stream, _lib.moe_expert_matmul, ctypes.byref(shape.c()),
+         ctypes.byref(linear.c()), _ptr(x), _ptr(x_scales), _maybe(lay), _ptr(weight),
+         _ptr(weight_scales), _ptr(bias), _ptr(residual), _ptr(y), _ptr(pre))
+
+
+def moe_expert_matmul_backward_workspace_size(shape: Shape, linear: Linear) -> int:
+    return int(_lib.moe_expert_matmul_backward_workspace_size(ctypes.byref(shape.c()),
+                                                              ctypes.byref(linear.c())))
+
+
+def alloc_expert_workspace(shape: Shape, linear: Linear, device) -> Optional[torch.Tensor]:
+    """Workspace of moe_expert_matmul_backward (None when none is needed)."""
+    n = moe_expert_matmul_backward_workspace_size(shape, linear)
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_expert_matmul_backward(shape: Shape, linear: Linear, grad_y: torch.Tensor,
+                               x: Optional[torch.Tensor], layout: Optional[Layout],
+                               weight: Optional[torch.Tensor], pre: Optional[torch.Tensor],
+                               grad_x: Optional[torch.Tensor],
+                               grad_weight: Optional[torch.Tensor],
+                               grad_bias: Optional[torch.Tensor],
+                               workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_expert_matmul (bf16); any of the three outputs may be None."""
+    c, dev = "moe_expert_matmul_backward", -1
+    rows = _rows(shape)
+    if rows is not None:
+        E, K, F, P = shape.num_experts, linear.in_features, linear.out_features, linear.pre_features
+        rows = rows if layout is not None else shape.num_tokens
+        dev = _all(c, (("grad_y", grad_y, _BF16, rows * F, True),
+                       ("x", x, _BF16, rows * K, grad_weight is not None),
+                       ("weight", weight, _BF16, E * P * K, grad_x is not None),
+                       ("pre", pre, _BF16, rows * P, linear.activation != MOE_ACT_NONE),
+                       ("grad_x", grad_x, _BF16, rows * K, False),
+                       ("grad_weight", grad_weight, _BF16, E * P * K, False),
+                       ("grad_bias", grad_bias, _F32, E * P, False),
+                       ("workspace", workspace, _BYTES, 0, False), *_segments(shape, layout)))
+    lay = None if layout is None else layout.c()
+    _run(c, dev, stream, _lib.moe_expert_matmul_backward, ctypes.byref(shape.c()),
+         ctypes.byref(linear.c()), _ptr(grad_y), _ptr(x), _maybe(lay), _ptr(weight), _ptr(pre),
+         _ptr(grad_x), _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace), _nbytes(workspace))
+
+
+def moe_combine_backward(shape: Shape, grad_out: torch.Tensor, expert_y: Optional[torch.Tensor],
+                         layout: Layout, topk_weights: Optional[torch.Tensor],
+                         grad_y: Optional[torch.Tensor], grad_weights: Optional[torch.Tensor],
+                         stream=None) -> None:
+    """Gradients of moe_combine (bf16); either output may be None."""
+    c, dev = "moe_combine_backward", -1
+    rows = _rows(shape)
+    if rows is not None:
+        if layout is None:
+            raise ValueError(f"{c}: layout is required")
+        T, H, k = shape.num_tokens, shape.hidden, shape.top_k
+        dev = _all(c, (("grad_out", grad_out, _BF16, T * H, True),
+                       ("expert_y", expert_y, _BF16, rows * H, grad_weights is not None),
+                       ("layout.token_row", layout.token_row, _I32, T * k, True),
+                       ("topk_weights", topk_weights, _F32, T * k, grad_y is not None),
+                       ("grad_y", grad_y, _BF16, rows * H, False),
+                       ("grad_weights", grad_weights, _F32, T * k, False)))
+    _run(c, dev, stream, _lib.moe_combine_backward, ctypes.byref(shape.c()), _ptr(grad_out),
+         _ptr(expert_y), ctypes.byref(layout.c()), _ptr(topk_weights), _ptr(grad_y),
+         _ptr(grad_weights))
+
+
+def moe_balance_loss_workspace_size(T: int, E: int, num_seqs: int) -> int:
+    return int(_lib.moe_balance_loss_workspace_size(T, E, num_seqs))
+
+
+def moe_balance_loss(logits: torch.Tensor, bias: Optional[torch.Tensor], topk_ids: torch.Tensor,
+                     score: int, coef: float, seq_offsets: Optional[torch.Tensor] = None,
+                     expert_counts: Optional[torch.Tensor] = None,
+                     expert_probs: Optional[torch.Tensor] = None,
+                     seq_tokens: Optional[torch.Tensor] = None,
+                     loss: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Balance loss of a routed batch; returns (loss [1], expert_counts [S,E],
+    expert_probs [S,E], seq_tokens [S])."""
+    c = "moe_balance_loss"
+    T, E, k = _router_sizes(c, logits, topk_ids)
+    S = _num_seqs(c, seq_offsets)
+    dev = logits.device
+    if expert_counts is None:
+        expert_counts = torch.empty(S, E, dtype=torch.int32, device=dev)
+    if expert_probs is None:
+        expert_probs = torch.empty(S, E, dtype=torch.float32, device=dev)
+    if seq_tokens is None:
+        seq_tokens = torch.empty(S, dtype=torch.int32, device=dev)
+    if loss is None:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+    d = _all(c, (("logits", logits, _F32, T * E, True), ("bias", bias, _F32, E, False),
+                 ("topk_ids", topk_ids, _I32, T * k, True),
+                 ("seq_offsets", seq_offsets, _I32, S + 1, False),
+                 ("expert_counts", expert_counts, _I32, S * E, True),
+                 ("expert_probs", expert_probs, _F32, S * E, True),
+                 ("seq_tokens", seq_tokens, _I32, S, True), ("loss", loss, _F32, 1, True),
+                 ("workspace", workspace, _BYTES, 0, False)))
+    ws = _workspace(_lib.moe_balance_loss_workspace_size(T, E, S), workspace, d, stream, c)
+    _run(c, d, stream, _lib.moe_balance_loss, _ptr(logits), _ptr(bias), _ptr(topk_ids), T, E, k,
+         score, _ptr(seq_offsets), S, coef, _ptr(expert_counts), _ptr(expert_probs),
+         _ptr(seq_tokens), _ptr(loss), _ptr(ws), _nbytes(ws))
+    return loss, expert_counts, expert_probs, seq_tokens
+
+
+def moe_route_backward_workspace_size(T: int, E: int) -> int:
+    return int(_lib.moe_route_backward_workspace_size(T, E))
+
+
+def moe_route_backward(logits: torch.Tensor, bias: Optional[torch.Tensor], topk_ids: torch.Tensor,
+                       topk_weights: Optional[torch.Tensor],
+                       grad_weights: Optional[torch.Tensor], score: int, coef: float = 0.0,
+                       seq_offsets: Optional[torch.Tensor] = None,
+                       expert_counts: Optional[torch.Tensor] = None,
+                       seq_tokens: Optional[torch.Tensor] = None,
+                       grad_loss: Optional[torch.Tensor] = None,
+                       grad_logits: Optional[torch.Tensor] = None,
+                       grad_bias: Optional[torch.Tensor] = None, with_grad_bias: bool = False,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of the router's logits; returns (grad_logits [T,E], grad_bias [E]
+    or None).  with_grad_bias: allocate grad_bias when none is given."""
+    c = "moe_route_backward"
+    T, E, k = _router_sizes(c, logits, topk_ids)
+    S = _num_seqs(c, seq_offsets)
+    dev = logits.device
+    if grad_logits is None:
+        grad_logits = torch.empty(T, E, dtype=torch.float32, device=dev)
+    if grad_bias is None and with_grad_bias:
+        grad_bias = torch.empty(E, dtype=torch.float32, device=dev)
+    d = _all(c, (("logits", logits, _F32, T * E, True), ("bias", bias, _F32, E, False),
+                 ("topk_ids", topk_ids, _I32, T * k, True),
+                 ("topk_weights", topk_weights, _F32, T * k, grad_weights is not None),
+                 ("grad_weights", grad_weights, _F32, T * k, False),
+                 ("seq_offsets", seq_offsets, _I32, S + 1, False),
+                 ("expert_counts", expert_counts, _I32, S * E, False),
+                 ("seq_tokens", seq_tokens, _I32, S, False),
+                 ("grad_loss", grad_loss, _F32, 1, False),
+                 ("grad_logits", grad_logits, _F32, T * E, True),
+                 ("grad_bias", grad_bias, _F32, E, False),
+                 ("workspace", workspace, _BYTES, 0, False)))
+    need = 0 if grad_bias is None else _lib.moe_route_backward_workspace_size(T, E)
+    ws = _workspace(need, workspace, d, stream, c)
+    _run(c, d, stream, _lib.moe_route_backward, _ptr(logits), _ptr(bias), _ptr(topk_ids),
+         _ptr(topk_weights), _ptr(grad_weights), T, E, k, score, _ptr(seq_offsets), S, coef,
+         _ptr(expert_counts), _ptr(seq_tokens), _ptr(grad_loss), _ptr(grad_logits),
+         _ptr(grad_bias), _ptr(ws), _nbytes(ws))
+    return grad_logits, grad_bias
+
+
+def _router_sizes(call, logits, topk_ids):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError(f"{call}: logits must be a 2-D tensor [T, E]")
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2 or \
+            topk_ids.shape[0] != logits.shape[0]:
+        raise ValueError(f"{call}: topk_ids must be a 2-D tensor [T, k]")
+    return logits.shape[0], logits.shape[1], topk_ids.shape[1]
+
+
+def _num_seqs(call, seq_offsets) -> int:
+    if seq_offsets is None:
+        return 1
+    if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1:
+        raise ValueError(f"{call}: seq_offsets must be a 1-D tensor [S + 1]")
+    if seq_offsets.numel() < 2:
+        raise ValueError(f"{call}: seq_offsets must hold one sequence at least")
+    return seq_offsets.numel() - 1

@@ -21,7 +21,8 @@ CEILING_SOURCE = "ceiling.hip"
 TRACE_LIB = os.path.join(HERE, "libmoe_trace.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["capi.hip", "route_topk.hip", "dispatch.hip", "sources.hip", "combine.hip",
-           "combine_partial.hip", "gemm_io.hip", "expert_scale.hip", "dispatch_static.hip"]
+           "combine_partial.hip", "gemm_io.hip", "expert_scale.hip", "dispatch_static.hip",
+           "capi_experts.hip", "expert_matmul.hip", "combine_grad.hip", "balance.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

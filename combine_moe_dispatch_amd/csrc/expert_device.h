@@ -1,0 +1,40 @@
+// expert_device.h -- device helpers of the expert product and its gradient.
+#pragma once
+
+#include "device_common.h"
+#include "experts.h"
+
+namespace moe {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActSwiglu = 3 };
+
+__device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// Rows [begin, end) of expert e that hold placed pairs: its counts cut at its
+// rank's capacity, and at the buffer whatever the metadata says.
+__device__ __forceinline__ void segment_of(const Segments& s, int e, int& begin, int& end) {
+  if (s.counts == nullptr) {
+    begin = 0;
+    end = s.rows;
+    return;
+  }
+  begin = max(s.offsets[e], 0);
+  int64_t last = (int64_t)begin + max(s.counts[e], 0);
+  if (s.C > 0) last = min(last, (int64_t)(e / s.L) * s.C + s.C);
+  end = (int)min(last, (int64_t)s.rows);
+}
+
+__device__ __forceinline__ float sigmoid_f32(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+// act(z) for the one-input activations
+template <int ACT>
+__device__ __forceinline__ float act_f32(float z) {
+  if (ACT == kActSilu) return z * sigmoid_f32(z);
+  if (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  return z;
+}
+
+}  // namespace moe
