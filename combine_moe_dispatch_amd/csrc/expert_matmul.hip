@@ -12,44 +12,144 @@
 //   y      u = weight row,     v = token row,  r = input feature
 //   grad_x u = input feature,  v = token row,  r = weight row (A transposed)
 //   grad_w u = input feature,  v = weight row, r = token row (both transposed)
-// A block of four waves holds a 64 x 64 tile of D; the operands pass through
-// LDS in steps of 32 along r, zeros past their ends.
-#include "expert_device.h"
+// so that a lane's four accumulators are neighbours in memory.  A block holds
+// a tile of D in registers and walks r in steps of 64: while its eight waves
+// multiply one step out of LDS, the loads of the next go straight into the
+// other half of it.
+#include <type_traits>
+
+#include "expert_tile.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kStep = 32;
-constexpr int kPitch = kStep + 8;
+constexpr int kTile = 64;   // fp8: tile and step of the product over widened codes
+constexpr int kCodes = 32;
+constexpr int kPitch = kCodes + 8;
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-
-// 64 x 32 operand tile, rows i0.., columns r0.. of a row-major matrix (ld
-// elements a row), zeros past rows/red.
-__device__ __forceinline__ void stage_rows(uint16_t (*s)[kPitch], const uint16_t* m, size_t ld,
-                                           int i0, int i_end, int r0, int red) {
-  const int i = threadIdx.x / 4, c = (threadIdx.x % 4) * 8;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (i0 + i < i_end && r0 + c < red) v = load16(m + (size_t)(i0 + i) * ld + r0 + c);
-  *reinterpret_cast<uint4*>(&s[i][c]) = v;
+__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// The same tile of a matrix that holds it transposed: row r, column i.
-__device__ __forceinline__ void stage_cols(uint16_t (*s)[kPitch], const uint16_t* m, size_t ld,
-                                           int i0, int i_end, int r0, int red) {
-  const int r = threadIdx.x / 8, c = (threadIdx.x % 8) * 8;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (r0 + r < red && i0 + c < i_end) v = load16(m + (size_t)(r0 + r) * ld + i0 + c);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// ---------------------------------------------------------------------------
+// The tile product
+// ---------------------------------------------------------------------------
+// WU x WV waves of TU x TV fragments of 16 x 16.
+template <int WU, int WV, int TU, int TV>
+struct Config {
+  static constexpr int kWu = WU, kWv = WV, kTu = TU, kTv = TV;
+  static constexpr int kWaves = WU * WV, kThreads = kWaves * kWave;
+  static constexpr int kBu = WU * TU * 16, kBv = WV * TV * 16;
+};
+
+template <class C, bool AT, bool BT>
+struct TileProduct {
+  using A = OperandTile<C::kBu, C::kWaves, AT>;
+  using B = OperandTile<C::kBv, C::kWaves, BT>;
+  static constexpr int kStage = A::kBytes + B::kBytes;
+  A a;
+  B b;
+  f32x4_t acc[C::kTu][C::kTv];
+
+  typename A::template Reader<C::kTu> ra;
+  typename B::template Reader<C::kTv> rb;
+
+  template <bool TAIL>
+  __device__ __forceinline__ void multiply(uint32_t sa, uint32_t sb, int left) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    s[c + 2 * e][r] = (uint16_t)w[e];
-    s[c + 2 * e + 1][r] = (uint16_t)(w[e] >> 16);
+    for (int ks = 0; ks < kStep / 32; ++ks) {
+      bf16x8_t fa[C::kTu], fb[C::kTv];
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) fb[v] = rb.template frag<TAIL>(sb, v, ks, left);
+#pragma unroll
+      for (int u = 0; u < C::kTu; ++u) fa[u] = ra.template frag<TAIL>(sa, u, ks, left);
+#pragma unroll
+      for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+        for (int v = 0; v < C::kTv; ++v)
+          acc[u][v] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u], fb[v], acc[u][v], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-}
+
+  // red > 0 positions along r.  ap[i] is where load i of this wave starts in A
+  // (weight rows of a gated layer lie in two places), bp in B; lda, ldb are
+  // the operands' row pitches in bytes.
+  __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
+                                      const char* bp, uint32_t lda, uint32_t ldb, int red) {
+    ra.init(wave % C::kWu * C::kTu * 16);
+    rb.init(wave / C::kWu * C::kTv * 16);
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const size_t sta = AT ? (size_t)kStep * lda : (size_t)kStep * 2;
+    const size_t stb = BT ? (size_t)kStep * ldb : (size_t)kStep * 2;
+    const uint32_t lds = lds_address(smem);
+    const int full = red / kStep, left = red % kStep;  // whole steps, rest
+    uint32_t here = lds, next = lds + kStage;
+    auto start = [&](uint32_t to, auto tail) {
+      load<decltype(tail)::value>(to, to + A::kBytes, wave, ap, bp, lda, ldb, left);
+#pragma unroll
+      for (int i = 0; i < A::kLoads; ++i) ap[i] += sta;
+      bp += stb;
+    };
+    auto swap = [&] {
+      wait_lds();  // this wave's reads are done before the others may overwrite
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const uint32_t h = here;
+      here = next;
+      next = h;
+    };
+    auto ready = [&] {  // every wave's loads of this step are in LDS
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    const std::false_type whole{};
+    const std::true_type rest{};
+    if (full > 0) start(here, whole);
+    for (int t = 0; t + 1 < full; ++t) {
+      start(next, whole);
+      wait_vm<A::kLoads + B::kLoads>();
+      ready();
+      multiply<false>(here, here + A::kBytes, left);
+      swap();
+    }
+    if (full > 0) {
+      if (left > 0) {
+        start(next, rest);
+        wait_vm<A::kLoads + B::kLoads>();
+      } else {
+        wait_vm<0>();
+      }
+      ready();
+      multiply<false>(here, here + A::kBytes, left);
+      swap();
+    } else {
+      start(here, rest);
+    }
+    if (left > 0) {
+      wait_vm<0>();
+      ready();
+      multiply<true>(here, here + A::kBytes, left);
+    }
+  }
+
+  template <bool TAIL>
+  __device__ __forceinline__ void load(uint32_t sa, uint32_t sb, int wave,
+                                       const char* (&ap)[A::kLoads], const char* bp, uint32_t lda,
+                                       uint32_t ldb, int left) const {
+    a.template load<TAIL>(sa, wave, ap, lda, left);
+    const char* bs[B::kLoads];
+#pragma unroll
+    for (int i = 0; i < B::kLoads; ++i) bs[i] = bp;
+    b.template load<TAIL>(sb, wave, bs, ldb, left);
+  }
+};
 
 // e4m3 codes widened to bf16 (exact).
 __device__ __forceinline__ void stage_codes(uint16_t (*s)[kPitch], const uint8_t* m, size_t ld,
@@ -78,13 +178,9 @@ __device__ __forceinline__ void mma_step(f32x4_t (&acc)[4], uint16_t (*sa)[kPitc
     acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sa, u * 16), b, acc[u], 0, 0, 0);
 }
 
-__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
-
-template <bool FP8, int ACT>
+template <int ACT>
 __global__ void __launch_bounds__(kThreads)
-matmul_kernel(MatmulParams p) {
+matmul_fp8_kernel(MatmulParams p) {
   __shared__ __align__(16) uint16_t sa[kTile][kPitch], sb[kTile][kPitch];
   constexpr bool kGated = ACT == kActSwiglu;
   constexpr int kCols = kGated ? kTile / 2 : kTile;  // output columns of a block
@@ -98,46 +194,31 @@ matmul_kernel(MatmulParams p) {
   const int col = n0 + (kGated ? srow % kCols : srow);
   const int wrow = col < p.F ? (kGated && srow >= kCols ? p.F + col : col) : -1;
   for (int m0 = begin; m0 < end; m0 += kTile) {
+    const int m = m0 + (threadIdx.x / kWave) * 16 + (lane & 15);
     f32x4_t acc[4] = {};
-    if constexpr (FP8) {
-      const uint8_t* w = static_cast<const uint8_t*>(p.weight) + (size_t)e * p.P * p.K;
-      const uint8_t* x = static_cast<const uint8_t*>(p.x);
-      const int kb = p.K / 128;
-      const int m = m0 + (threadIdx.x / kWave) * 16 + (lane & 15);
-      for (int b = 0; b < kb; ++b) {
-        f32x4_t part[4] = {};
-        for (int r0 = b * 128; r0 < b * 128 + 128; r0 += kStep) {
-          __syncthreads();
-          stage_codes(sa, w, p.K, max(wrow, 0), wrow >= 0, r0);
-          stage_codes(sb, x, p.K, min(m0 + srow, end - 1), m0 + srow < end, r0);
-          __syncthreads();
-          mma_step(part, sa, sb);
-        }
-        const float sx = m < end ? p.x_scales[(size_t)m * kb + b] : 0.0f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = n0 + (kGated ? (u % 2) * 16 : u * 16) + (lane >> 4) * 4;
-          const int row = min(c, p.F - 1) + (kGated && u >= 2 ? p.F : 0);
-          const float s =
-              sx * p.weight_scales[((size_t)e * (p.P / 128) + row / 128) * kb + b];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[u][i] = fmaf(part[u][i], s, acc[u][i]);
-        }
+    const uint8_t* w = static_cast<const uint8_t*>(p.weight) + (size_t)e * p.P * p.K;
+    const uint8_t* x = static_cast<const uint8_t*>(p.x);
+    const int kb = p.K / 128;
+    for (int b = 0; b < kb; ++b) {
+      f32x4_t part[4] = {};
+      for (int r0 = b * 128; r0 < b * 128 + 128; r0 += kCodes) {
+        __syncthreads();
+        stage_codes(sa, w, p.K, max(wrow, 0), wrow >= 0, r0);
+        stage_codes(sb, x, p.K, min(m0 + srow, end - 1), m0 + srow < end, r0);
+        __syncthreads();
+        mma_step(part, sa, sb);
       }
-    } else {
-      const uint16_t* w = static_cast<const uint16_t*>(p.weight) + (size_t)e * p.P * p.K;
-      for (int r0 = 0; r0 < p.K; r0 += kStep) {
-        __syncthreads();
-        const int c = (threadIdx.x % 4) * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (wrow >= 0 && r0 + c < p.K) v = load16(w + (size_t)wrow * p.K + r0 + c);
-        *reinterpret_cast<uint4*>(&sa[srow][c]) = v;
-        stage_rows(sb, static_cast<const uint16_t*>(p.x), p.K, m0, end, r0, p.K);
-        __syncthreads();
-        mma_step(acc, sa, sb);
+      const float sx = m < end ? p.x_scales[(size_t)m * kb + b] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = n0 + (kGated ? (u % 2) * 16 : u * 16) + (lane >> 4) * 4;
+        const int row = min(c, p.F - 1) + (kGated && u >= 2 ? p.F : 0);
+        const float s =
+            sx * p.weight_scales[((size_t)e * (p.P / 128) + row / 128) * kb + b];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[u][i] = fmaf(part[u][i], s, acc[u][i]);
       }
     }
-    const int m = m0 + (threadIdx.x / kWave) * 16 + (lane & 15);
     if (m >= end) continue;
     float z[4][4];
     int cols[4];
@@ -215,79 +296,250 @@ act_grad_kernel(MatmulGradParams p, uint16_t* gz) {
   }
 }
 
-// grad_x: D[input feature][token row], A transposed.
-__global__ void __launch_bounds__(kThreads)
-grad_x_kernel(MatmulGradParams p, const uint16_t* gz) {
-  __shared__ __align__(16) uint16_t sa[kTile][kPitch], sb[kTile][kPitch];
-  const int e = blockIdx.y, n0 = blockIdx.x * kTile, lane = lane_id();
-  int begin, end;
-  segment_of(p.seg, e, begin, end);
-  const uint16_t* w = p.weight + (size_t)e * p.P * p.K;
-  for (int m0 = begin; m0 < end; m0 += kTile) {
-    f32x4_t acc[4] = {};
-    for (int r0 = 0; r0 < p.P; r0 += kStep) {
-      __syncthreads();
-      stage_cols(sa, w, p.K, n0, p.K, r0, p.P);
-      stage_rows(sb, gz, p.P, m0, end, r0, p.P);
-      __syncthreads();
-      mma_step(acc, sa, sb);
-    }
-    const int m = m0 + (threadIdx.x / kWave) * 16 + (lane & 15);
-    if (m >= end) continue;
+// y (and pre): u runs over weight rows; a gated layer's wave takes half of its
+// fragments from the gate rows and half from the up rows of the same columns.
+template <class C, int ACT>
+__global__ void __launch_bounds__(C::kThreads)
+matmul_kernel(MatmulParams p, int ntiles) {
+  using Product = TileProduct<C, false, false>;
+  constexpr bool kGated = ACT == kActSwiglu;
+  constexpr int kCols = kGated ? C::kBu / 2 : C::kBu;   // output columns of a tile
+  constexpr int kWaveCols = kCols / C::kWu;             // and of a wave
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = lane_id();
+  const int n0 = t.n * kCols;
+  const uint32_t ld = (uint32_t)p.K * 2;
+  const char* w = static_cast<const char*>(p.weight) + (size_t)t.e * p.P * ld;
+  Product prod;
+  // weight row behind tile row j: of a gated wave's rows the first half are
+  // gate rows, the second half the up rows of the same columns
+  const char* ap[Product::A::kLoads];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = n0 + u * 16 + (lane >> 4) * 4;
-      const float v[4] = {acc[u][0], acc[u][1], acc[u][2], acc[u][3]};
-      if (c < p.K) store4(p.grad_x + (size_t)m * p.K + c, v);
+  for (int i = 0; i < Product::A::kLoads; ++i) {
+    const int q = wave * Product::A::kLoads + i;
+    const int row = q * 8 + lane / 8;
+    int col = row;
+    bool up = false;
+    if (kGated) {
+      const int j = row % (2 * kWaveCols);
+      up = q * 8 % (2 * kWaveCols) >= kWaveCols;
+      col = row / (2 * kWaveCols) * kWaveCols + j % kWaveCols;
+    }
+    const int c = (lane % 8) ^ Product::A::swizzle(row);
+    prod.a.off[i] = (uint32_t)min(col, p.F - 1 - n0) * ld + (uint32_t)c * 16;
+    prod.a.where[i] = (uint16_t)(c * 8);
+    ap[i] = w + (size_t)(n0 + (up ? p.F : 0)) * ld;
+  }
+  prod.b.init(wave, ld, min(C::kBv, t.end - t.m0));
+  prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, ld, ld, p.K);
+
+  const int wu = wave % C::kWu, wv = wave / C::kWu;
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int m = t.m0 + (wv * C::kTv + v) * 16 + (lane & 15);
+    if (m >= t.end) continue;
+#pragma unroll
+    for (int u = 0; u < (kGated ? C::kTu / 2 : C::kTu); ++u) {
+      const int col = n0 + wu * kWaveCols + u * 16 + (lane >> 4) * 4;
+      if (col >= p.F) continue;
+      float z[4], up[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[i] = prod.acc[u][v][i];
+        up[i] = kGated ? prod.acc[(u + C::kTu / 2) % C::kTu][v][i] : 0.0f;
+      }
+      if (p.bias) {
+        const float* b = p.bias + (size_t)t.e * p.P + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[i] += b[i];
+          if (kGated) up[i] += b[p.F + i];
+        }
+      }
+      if (p.pre) {
+        store4(p.pre + (size_t)m * p.P + col, z);
+        if (kGated) store4(p.pre + (size_t)m * p.P + p.F + col, up);
+      }
+      float o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = kGated ? z[i] * sigmoid_f32(z[i]) * up[i] : act_f32<ACT>(z[i]);
+      const size_t at = (size_t)m * p.F + col;
+      if (p.residual) {
+        const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
+        o[0] += bf16_lo(r.x);
+        o[1] += bf16_hi(r.x);
+        o[2] += bf16_lo(r.y);
+        o[3] += bf16_hi(r.y);
+      }
+      store4(p.y + at, o);
     }
   }
 }
 
-// grad_w: D[input feature][weight row], both transposed, summed over rows.
-__global__ void __launch_bounds__(kThreads)
-grad_w_kernel(MatmulGradParams p, const uint16_t* gz) {
-  __shared__ __align__(16) uint16_t sa[kTile][kPitch], sb[kTile][kPitch];
-  const int e = blockIdx.z, n0 = blockIdx.x * kTile, p0 = blockIdx.y * kTile, lane = lane_id();
-  int begin, end;
-  segment_of(p.seg, e, begin, end);
-  f32x4_t acc[4] = {};
-  for (int r0 = begin; r0 < end; r0 += kStep) {
-    __syncthreads();
-    stage_cols(sa, p.x, p.K, n0, p.K, r0, end);
-    stage_cols(sb, gz, p.P, p0, p.P, r0, end);
-    __syncthreads();
-    mma_step(acc, sa, sb);
-  }
-  const int row = p0 + (threadIdx.x / kWave) * 16 + (lane & 15);
-  if (row >= p.P) return;
+// grad_x: D[input feature][token row].
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+grad_x_kernel(MatmulGradParams p, const uint16_t* gz, int ntiles) {
+  using Product = TileProduct<C, true, false>;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = lane_id();
+  const int n0 = t.n * C::kBu;
+  const uint32_t lda = (uint32_t)p.K * 2, ldb = (uint32_t)p.P * 2;
+  Product prod;
+  prod.a.init(wave, lda, min(C::kBu, p.K - n0));
+  prod.b.init(wave, ldb, min(C::kBv, t.end - t.m0));
+  const char* ap[Product::A::kLoads];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int c = n0 + u * 16 + (lane >> 4) * 4;
-    const float v[4] = {acc[u][0], acc[u][1], acc[u][2], acc[u][3]};
-    if (c < p.K) store4(p.grad_weight + ((size_t)e * p.P + row) * p.K + c, v);
+  for (int i = 0; i < Product::A::kLoads; ++i)
+    ap[i] = reinterpret_cast<const char*>(p.weight + (size_t)t.e * p.P * p.K + n0);
+  prod.run(smem, wave, ap, reinterpret_cast<const char*>(gz) + (size_t)t.m0 * ldb, lda, ldb, p.P);
+  const int wu = wave % C::kWu, wv = wave / C::kWu;
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int m = t.m0 + (wv * C::kTv + v) * 16 + (lane & 15);
+    if (m >= t.end) continue;
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u) {
+      const int c = n0 + (wu * C::kTu + u) * 16 + (lane >> 4) * 4;
+      const float o[4] = {prod.acc[u][v][0], prod.acc[u][v][1], prod.acc[u][v][2],
+                          prod.acc[u][v][3]};
+      if (c < p.K) store4(p.grad_x + (size_t)m * p.K + c, o);
+    }
   }
 }
 
-template <bool FP8>
-void launch_forward(const MatmulParams& p, hipStream_t st) {
-  const int cols = p.act == kActSwiglu ? kTile / 2 : kTile;
-  const dim3 grid((p.F + cols - 1) / cols, p.seg.E);
-  switch (p.act) {
-    case kActSilu: hipLaunchKernelGGL((matmul_kernel<FP8, kActSilu>), grid, dim3(kThreads), 0, st, p); break;
-    case kActGelu: hipLaunchKernelGGL((matmul_kernel<FP8, kActGelu>), grid, dim3(kThreads), 0, st, p); break;
-    case kActSwiglu: hipLaunchKernelGGL((matmul_kernel<FP8, kActSwiglu>), grid, dim3(kThreads), 0, st, p); break;
-    default: hipLaunchKernelGGL((matmul_kernel<FP8, kActNone>), grid, dim3(kThreads), 0, st, p); break;
+// grad_w: D[input feature][weight row], summed over the expert's rows.
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+grad_w_kernel(MatmulGradParams p, const uint16_t* gz, unsigned nt, unsigned pt) {
+  using Product = TileProduct<C, true, true>;
+  extern __shared__ __align__(1024) char smem[];
+  const unsigned b = xcd_local_block(blockIdx.x, gridDim.x);
+  const int e = (int)(b / (nt * pt));
+  const unsigned in = b % (nt * pt);
+  const int n0 = (int)(in / pt) * C::kBu, p0 = (int)(in % pt) * C::kBv;
+  int begin, end;
+  segment_of(p.seg, e, begin, end);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = lane_id();
+  const uint32_t lda = (uint32_t)p.K * 2, ldb = (uint32_t)p.P * 2;
+  Product prod;
+  if (end > begin) {
+    prod.a.init(wave, lda, min(C::kBu, p.K - n0));
+    prod.b.init(wave, ldb, min(C::kBv, p.P - p0));
+    const char* ap[Product::A::kLoads];
+#pragma unroll
+    for (int i = 0; i < Product::A::kLoads; ++i)
+      ap[i] = reinterpret_cast<const char*>(p.x + (size_t)begin * p.K + n0);
+    prod.run(smem, wave, ap, reinterpret_cast<const char*>(gz + (size_t)begin * p.P + p0), lda,
+             ldb, end - begin);
+  } else {
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) prod.acc[u][v] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  const int wu = wave % C::kWu, wv = wave / C::kWu;
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int row = p0 + (wv * C::kTv + v) * 16 + (lane & 15);
+    if (row >= p.P) continue;
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u) {
+      const int c = n0 + (wu * C::kTu + u) * 16 + (lane >> 4) * 4;
+      const float o[4] = {prod.acc[u][v][0], prod.acc[u][v][1], prod.acc[u][v][2],
+                          prod.acc[u][v][3]};
+      if (c < p.K) store4(p.grad_weight + ((size_t)e * p.P + row) * p.K + c, o);
+    }
+  }
+}
+
+// 256 x 256 tiles for experts of many rows, 256 x 128 for those of few: a part
+// tile wastes the products of its missing rows.
+using Large = Config<2, 4, 8, 4>;
+using Small = Config<4, 2, 4, 4>;
+
+// Large tiles where an expert has more rows than one small tile on average
+// and the large tiles alone fill the 256 compute units.
+bool large_tiles(const Segments& s, int u) {
+  const int64_t tiles = ((int64_t)s.pairs / Large::kBv) * ((u + Large::kBu - 1) / Large::kBu);
+  return s.pairs / s.E > Small::kBv && tiles >= 256;
+}
+
+template <class K>
+hipError_t allow_lds(K kernel, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <class C, int ACT>
+hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
+  constexpr int kCols = ACT == kActSwiglu ? C::kBu / 2 : C::kBu;
+  constexpr int kLds = 2 * TileProduct<C, false, false>::kStage;
+  const int ntiles = (p.F + kCols - 1) / kCols;
+  const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  const hipError_t e = allow_lds(matmul_kernel<C, ACT>, kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((matmul_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p,
+                     ntiles);
+  return hipGetLastError();
+}
+
+template <int ACT>
+hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
+  if (fp8) {
+    const int cols = ACT == kActSwiglu ? kTile / 2 : kTile;
+    hipLaunchKernelGGL((matmul_fp8_kernel<ACT>), dim3((p.F + cols - 1) / cols, p.seg.E),
+                       dim3(kThreads), 0, st, p);
+    return hipGetLastError();
+  }
+  if (large_tiles(p.seg, p.P)) return launch_tiles<Large, ACT>(p, st);
+  return launch_tiles<Small, ACT>(p, st);
+}
+
+template <class C>
+hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStream_t st) {
+  constexpr int kLds = 2 * TileProduct<C, true, false>::kStage;
+  const int ntiles = (p.K + C::kBu - 1) / C::kBu;
+  const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  const hipError_t e = allow_lds(grad_x_kernel<C>, kLds);
+  if (e != hipSuccess || grid == 0) return e;
+  hipLaunchKernelGGL((grad_x_kernel<C>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p, gz,
+                     ntiles);
+  return hipGetLastError();
+}
+
+template <class C>
+hipError_t launch_grad_w(const MatmulGradParams& p, const uint16_t* gz, hipStream_t st) {
+  constexpr int kLds = 2 * TileProduct<C, true, true>::kStage;
+  const unsigned nt = (p.K + C::kBu - 1) / C::kBu, pt = (p.P + C::kBv - 1) / C::kBv;
+  const int64_t grid = (int64_t)nt * pt * p.seg.E;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  const hipError_t e = allow_lds(grad_w_kernel<C>, kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((grad_w_kernel<C>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p, gz,
+                     nt, pt);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_expert_matmul(const MatmulParams& p, bool fp8, hipStream_t st) {
-  if (fp8)
-    launch_forward<true>(p, st);
-  else
-    launch_forward<false>(p, st);
-  return hipGetLastError();
+  switch (p.act) {
+    case kActSilu: return launch_forward<kActSilu>(p, fp8, st);
+    case kActGelu: return launch_forward<kActGelu>(p, fp8, st);
+    case kActSwiglu: return launch_forward<kActSwiglu>(p, fp8, st);
+    default: return launch_forward<kActNone>(p, fp8, st);
+  }
 }
 
 size_t expert_matmul_grad_workspace(int rows, int pairs, int E, int P, int act) {
@@ -306,12 +558,14 @@ hipError_t launch_expert_matmul_grad(const MatmulGradParams& p, hipStream_t st) 
     }
   }
   const uint16_t* g = gz ? gz : p.grad_y;
-  const unsigned nt = (p.K + kTile - 1) / kTile, pt = (p.P + kTile - 1) / kTile;
-  if (p.grad_x)
-    hipLaunchKernelGGL(grad_x_kernel, dim3(nt, p.seg.E), dim3(kThreads), 0, st, p, g);
-  if (p.grad_weight)
-    hipLaunchKernelGGL(grad_w_kernel, dim3(nt, pt, p.seg.E), dim3(kThreads), 0, st, p, g);
-  return hipGetLastError();
+  const bool large = large_tiles(p.seg, p.K);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && p.grad_x)
+    e = large ? launch_grad_x<Large>(p, g, st) : launch_grad_x<Small>(p, g, st);
+  if (e == hipSuccess && p.grad_weight)
+    e = (int64_t)p.K * p.P >= 256 * 256 ? launch_grad_w<Large>(p, g, st)
+                                        : launch_grad_w<Small>(p, g, st);
+  return e;
 }
 
 }  // namespace moe

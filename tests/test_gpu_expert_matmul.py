@@ -281,3 +281,30 @@ def test_long_offsets():
     ref.check(gx[C:C + T], grads[0], tol[0], "grad_x")
     ref.check(gw[1:], grads[1], tol[1], "grad_weight")
     assert (gw[0] == 0).all()
+
+
+@pytest.mark.parametrize("name,T,E,k,K,F", [
+    ("swiglu", 2100, 2, 1, 72, 11272), ("none", 1030, 1, 1, 128, 22016),
+    ("gelu", 900, 3, 2, 200, 16392),
+])
+def test_many_rows_and_columns(name, T, E, k, K, F):
+    """Enough rows per expert and columns for the largest tiles, ragged at both ends."""
+    run(T, E, k, 1, 0, K, F, name, seed=T)
+
+
+@pytest.mark.parametrize("name,T,E,K,F", [("silu", 1100, 2, 16392, 136), ("none", 2050, 4, 8200, 264)])
+def test_gradients_of_wide_inputs(name, T, E, K, F):
+    shape, lay, recv, _, spans = layout(T, E, 1, 1, 0, K, T)
+    w, _ = weights(E, F, K, T, False)
+    gen = torch.Generator().manual_seed(T)
+    gy = torch.randn(T, F, generator=gen).bfloat16().cuda()
+    pre = torch.randn(T, F, generator=gen).bfloat16().cuda()
+    gx, gw, gb = torch.empty_like(recv), torch.empty_like(w), torch.empty(E, F, device="cuda")
+    lin = api.Linear(K, F, ACT[name])
+    z = None if name == "none" else pre
+    api.moe_expert_matmul_backward(shape, lin, gy, recv, lay, w, z, gx, gw, gb,
+                                   api.alloc_expert_workspace(shape, lin, "cuda"))
+    want, tol = ref.matmul_grad(host(gy), host(recv), host(w), host(pre), spans, name)
+    for got, wanted, bound, what in zip((gx.view(torch.bfloat16), gw, gb), want, tol,
+                                        ("grad_x", "grad_weight", "grad_bias")):
+        ref.check(got, wanted, bound, what)
