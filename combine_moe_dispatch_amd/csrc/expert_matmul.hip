@@ -13,7 +13,7 @@
 //   grad_x u = input feature,  v = token row,  r = weight row (A transposed)
 //   grad_w u = input feature,  v = weight row, r = token row (both transposed)
 // so that a lane's four accumulators are neighbours in memory.  A block holds
-// a tile of D in registers and walks r in steps of 64: while its eight waves
+// a tile of D in registers and walks r in steps of 64: while its four waves
 // multiply one step out of LDS, the loads of the next go straight into the
 // other half of it.
 #include <type_traits>
@@ -46,33 +46,54 @@ struct Config {
 
 template <class C, bool AT, bool BT>
 struct TileProduct {
-  using A = OperandTile<C::kBu, C::kWaves, AT>;
-  using B = OperandTile<C::kBv, C::kWaves, BT>;
+  using A = OperandTile<C::kBu, C::kWaves, AT, true>;
+  using B = OperandTile<C::kBv, C::kWaves, BT, false>;
   static constexpr int kStage = A::kBytes + B::kBytes;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLoads = A::kLoads + B::kLoads;
+  struct Fragments {
+    bf16x8_t a[C::kTu], b[C::kTv];
+  };
   A a;
   B b;
   f32x4_t acc[C::kTu][C::kTv];
-
   typename A::template Reader<C::kTu> ra;
   typename B::template Reader<C::kTv> rb;
 
+  // Fragment i (of kTv + kTu) of part k of the step at lds.
   template <bool TAIL>
-  __device__ __forceinline__ void multiply(uint32_t sa, uint32_t sb, int left) {
+  __device__ __forceinline__ void read(Fragments& f, int i, uint32_t lds, int k, int left) const {
+    if (i < C::kTv)
+      f.b[i] = rb.template frag<TAIL>(lds + A::kBytes, i, k, left);
+    else
+      f.a[i - C::kTv] = ra.template frag<TAIL>(lds, i - C::kTv, k, left);
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void read_all(Fragments& f, uint32_t lds, int k, int left) const {
 #pragma unroll
-    for (int ks = 0; ks < kStep / 32; ++ks) {
-      bf16x8_t fa[C::kTu], fb[C::kTv];
+    for (int i = 0; i < C::kTv + C::kTu; ++i) read<TAIL>(f, i, lds, k, left);
+  }
+
+  // acc += f, row of fragments by row, with before(u) in front of row u: what
+  // it issues runs beside the products.
+  template <class Before>
+  __device__ __forceinline__ void multiply(const Fragments& f, Before before) {
 #pragma unroll
-      for (int v = 0; v < C::kTv; ++v) fb[v] = rb.template frag<TAIL>(sb, v, ks, left);
+    for (int u = 0; u < C::kTu; ++u) {
+      before(u);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < C::kTu; ++u) fa[u] = ra.template frag<TAIL>(sa, u, ks, left);
-#pragma unroll
-      for (int u = 0; u < C::kTu; ++u)
-#pragma unroll
-        for (int v = 0; v < C::kTv; ++v)
-          acc[u][v] =
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u], fb[v], acc[u][v], 0, 0, 0);
+      for (int v = 0; v < C::kTv; ++v)
+        mfma_in_place(acc[u][v], f.a[u], f.b[v]);
       __builtin_amdgcn_sched_barrier(0);
     }
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
   }
 
   // red > 0 positions along r.  ap[i] is where load i of this wave starts in A
@@ -80,74 +101,114 @@ struct TileProduct {
   // the operands' row pitches in bytes.
   __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
                                       const char* bp, uint32_t lda, uint32_t ldb, int red) {
+    static_assert(kParts == 2, "the parts are written out");
     ra.init(wave % C::kWu * C::kTu * 16);
     rb.init(wave / C::kWu * C::kTv * 16);
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u)
-#pragma unroll
-      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    clear();
     const size_t sta = AT ? (size_t)kStep * lda : (size_t)kStep * 2;
     const size_t stb = BT ? (size_t)kStep * ldb : (size_t)kStep * 2;
-    const uint32_t lds = lds_address(smem);
-    const int full = red / kStep, left = red % kStep;  // whole steps, rest
-    uint32_t here = lds, next = lds + kStage;
-    auto start = [&](uint32_t to, auto tail) {
-      load<decltype(tail)::value>(to, to + A::kBytes, wave, ap, bp, lda, ldb, left);
+    uint32_t here = lds_address(smem), next = here + kStage;
+    const int steps = (red + kStep - 1) / kStep;
+    const int rest = red - (steps - 1) * kStep;       // positions of the last step
+    const int whole = rest == kStep ? steps : steps - 1;
+    auto advance = [&] {
 #pragma unroll
       for (int i = 0; i < A::kLoads; ++i) ap[i] += sta;
       bp += stb;
     };
-    auto swap = [&] {
-      wait_lds();  // this wave's reads are done before the others may overwrite
+    auto load = [&](int i, uint32_t to, auto tail) {  // load i of the next step
+      if (i < A::kLoads)
+        a.template load<decltype(tail)::value>(i, to, wave, ap[i], lda, rest);
+      else if (i < kLoads)
+        b.template load<decltype(tail)::value>(i - A::kLoads, to + A::kBytes, wave, bp, ldb, rest);
+    };
+    auto start = [&](uint32_t to, bool full) {
+      if (full) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load(i, to, std::false_type{});
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load(i, to, std::true_type{});
+      }
+      advance();
+    };
+    // Every wave's reads of `here` are in registers and its loads of `next` in
+    // LDS: `here` may be filled again and `next` be read.
+    auto meet = [&] {
+      wait_lds();
+      wait_vm<0>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
+    };
+    auto turn = [&] {
       const uint32_t h = here;
       here = next;
       next = h;
     };
-    auto ready = [&] {  // every wave's loads of this step are in LDS
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+    constexpr int kReads = (2 * (C::kTu + C::kTv) + C::kTu - 1) / C::kTu;  // in the first rows
+    constexpr int kStarts = (kLoads + C::kTu - 1) / C::kTu;
+    auto reading = [&](Fragments& f, uint32_t lds, int k, int u) {
+#pragma unroll
+      for (int i = u * kReads; i < (u + 1) * kReads; ++i)
+        if (i < C::kTu + C::kTv) read<false>(f, i, lds, k, rest);
     };
-    const std::false_type whole{};
-    const std::true_type rest{};
-    if (full > 0) start(here, whole);
-    for (int t = 0; t + 1 < full; ++t) {
-      start(next, whole);
-      wait_vm<A::kLoads + B::kLoads>();
-      ready();
-      multiply<false>(here, here + A::kBytes, left);
-      swap();
-    }
-    if (full > 0) {
-      if (left > 0) {
-        start(next, rest);
-        wait_vm<A::kLoads + B::kLoads>();
-      } else {
-        wait_vm<0>();
-      }
-      ready();
-      multiply<false>(here, here + A::kBytes, left);
-      swap();
+    const auto nothing = [](int) {};
+    Fragments f0, f1;
+    start(here, whole > 0);
+    if (steps > 1) {
+      start(next, whole > 1);
+      wait_vm<kLoads>();
     } else {
-      start(here, rest);
-    }
-    if (left > 0) {
       wait_vm<0>();
-      ready();
-      multiply<true>(here, here + A::kBytes, left);
     }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (steps > 1)
+      read_all<false>(f0, here, 0, rest);
+    else
+      read_all<true>(f0, here, 0, rest);
+    // Half a step is multiplied while the next half is read, the second half
+    // behind the barrier, so that the matrix units have work on both sides.
+    for (int t = 0; t + 2 < whole; ++t) {
+      multiply(f0, [&](int u) { reading(f1, here, 1, u); });
+      meet();
+      multiply(f1, [&](int u) {
+        reading(f0, next, 0, u);
+#pragma unroll
+        for (int i = u * kStarts; i < (u + 1) * kStarts; ++i) load(i, here, std::false_type{});
+      });
+      advance();
+      turn();
+    }
+    if (whole < steps && steps > 2) {  // the step whose loads are the short ones
+      multiply(f0, [&](int u) { reading(f1, here, 1, u); });
+      meet();
+      start(here, false);
+      multiply(f1, [&](int u) { reading(f0, next, 0, u); });
+      turn();
+    }
+    if (steps > 1) {
+      multiply(f0, [&](int u) { reading(f1, here, 1, u); });
+      meet();
+      multiply(f1, nothing);
+      read_all<true>(f0, next, 0, rest);
+      turn();
+    }
+    read_all<true>(f1, here, 1, rest);
+    multiply(f0, nothing);
+    multiply(f1, nothing);
+    mfma_results();
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) mfma_result(acc[u][v]);
   }
 
-  template <bool TAIL>
-  __device__ __forceinline__ void load(uint32_t sa, uint32_t sb, int wave,
-                                       const char* (&ap)[A::kLoads], const char* bp, uint32_t lda,
-                                       uint32_t ldb, int left) const {
-    a.template load<TAIL>(sa, wave, ap, lda, left);
-    const char* bs[B::kLoads];
+  // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours
+  // along u from a * 32 + (lane >> 4) * 8 on, of row v * 16 + (lane & 15).
+  __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
 #pragma unroll
-    for (int i = 0; i < B::kLoads; ++i) bs[i] = bp;
-    b.template load<TAIL>(sb, wave, bs, ldb, left);
+    for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
   }
 };
 
@@ -302,9 +363,11 @@ template <class C, int ACT>
 __global__ void __launch_bounds__(C::kThreads)
 matmul_kernel(MatmulParams p, int ntiles) {
   using Product = TileProduct<C, false, false>;
+  using A = typename Product::A;
   constexpr bool kGated = ACT == kActSwiglu;
-  constexpr int kCols = kGated ? C::kBu / 2 : C::kBu;   // output columns of a tile
-  constexpr int kWaveCols = kCols / C::kWu;             // and of a wave
+  constexpr int kPairs = (kGated ? C::kTu / 2 : C::kTu) / 2;  // along the output's columns
+  constexpr int kWaveCols = kPairs * 32;                // output columns of a wave
+  constexpr int kCols = kWaveCols * C::kWu;          // and of the tile
   extern __shared__ __align__(1024) char smem[];
   Tile t;
   if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
@@ -312,26 +375,23 @@ matmul_kernel(MatmulParams p, int ntiles) {
   const int lane = lane_id();
   const int n0 = t.n * kCols;
   const uint32_t ld = (uint32_t)p.K * 2;
-  const char* w = static_cast<const char*>(p.weight) + (size_t)t.e * p.P * ld;
+  const char* w = static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld;
   Product prod;
-  // weight row behind tile row j: of a gated wave's rows the first half are
-  // gate rows, the second half the up rows of the same columns
-  const char* ap[Product::A::kLoads];
+  const char* ap[A::kLoads];
 #pragma unroll
-  for (int i = 0; i < Product::A::kLoads; ++i) {
-    const int q = wave * Product::A::kLoads + i;
-    const int row = q * 8 + lane / 8;
-    int col = row;
-    bool up = false;
-    if (kGated) {
-      const int j = row % (2 * kWaveCols);
-      up = q * 8 % (2 * kWaveCols) >= kWaveCols;
-      col = row / (2 * kWaveCols) * kWaveCols + j % kWaveCols;
-    }
-    const int c = (lane % 8) ^ Product::A::swizzle(row);
+  for (int i = 0; i < A::kLoads; ++i) {
+    // the weight row behind tile row `row`: a gated wave's first rows are gate
+    // rows, the others the up rows of the same columns
+    const int q = wave * A::kLoads + i;
+    int row, c;
+    A::chunk_of(q, row, c);
+    const int first = q * A::kRowsPerLoad;  // the load's rows are of one kind
+    const bool up = kGated && first % (2 * kWaveCols) >= kWaveCols;
+    const int col =
+        kGated ? row / (2 * kWaveCols) * kWaveCols + row % kWaveCols : row;
     prod.a.off[i] = (uint32_t)min(col, p.F - 1 - n0) * ld + (uint32_t)c * 16;
     prod.a.where[i] = (uint16_t)(c * 8);
-    ap[i] = w + (size_t)(n0 + (up ? p.F : 0)) * ld;
+    ap[i] = w + (up ? (size_t)p.F * ld : 0);
   }
   prod.b.init(wave, ld, min(C::kBv, t.end - t.m0));
   prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, ld, ld, p.K);
@@ -342,40 +402,47 @@ matmul_kernel(MatmulParams p, int ntiles) {
     const int m = t.m0 + (wv * C::kTv + v) * 16 + (lane & 15);
     if (m >= t.end) continue;
 #pragma unroll
-    for (int u = 0; u < (kGated ? C::kTu / 2 : C::kTu); ++u) {
-      const int col = n0 + wu * kWaveCols + u * 16 + (lane >> 4) * 4;
+    for (int a = 0; a < kPairs; ++a) {
+      const int col = n0 + wu * kWaveCols + a * 32 + (lane >> 4) * 8;
       if (col >= p.F) continue;
-      float z[4], up[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[i] = prod.acc[u][v][i];
-        up[i] = kGated ? prod.acc[(u + C::kTu / 2) % C::kTu][v][i] : 0.0f;
-      }
+      float z[8], up[8];
+      prod.eight(z, a, v);
+      if (kGated) prod.eight(up, a + kPairs, v);
       if (p.bias) {
         const float* b = p.bias + (size_t)t.e * p.P + col;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[i] += b[i];
-          if (kGated) up[i] += b[p.F + i];
-        }
+        add8(z, b);
+        if (kGated) add8(up, b + p.F);
       }
       if (p.pre) {
-        store4(p.pre + (size_t)m * p.P + col, z);
-        if (kGated) store4(p.pre + (size_t)m * p.P + p.F + col, up);
+        store8(p.pre + (size_t)m * p.P + col, z);
+        if (kGated) store8(p.pre + (size_t)m * p.P + p.F + col, up);
       }
-      float o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = kGated ? z[i] * sigmoid_f32(z[i]) * up[i] : act_f32<ACT>(z[i]);
+      for (int i = 0; i < 8; ++i)
+        z[i] = kGated ? z[i] * sigmoid_f32(z[i]) * up[i] : act_f32<ACT>(z[i]);
       const size_t at = (size_t)m * p.F + col;
-      if (p.residual) {
-        const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
-        o[0] += bf16_lo(r.x);
-        o[1] += bf16_hi(r.x);
-        o[2] += bf16_lo(r.y);
-        o[3] += bf16_hi(r.y);
-      }
-      store4(p.y + at, o);
+      if (p.residual) add8(z, p.residual + at);
+      store8(p.y + at, z);
+    }
+  }
+}
+
+// The accumulators as bf16 rows: row v of the tile to out + v * ld, for v
+// below rows, columns below cols.
+template <class C, class Product>
+__device__ __forceinline__ void store_tile(const Product& prod, int wave, uint16_t* out, size_t ld,
+                                           int rows, int cols) {
+  const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int m = (wv * C::kTv + v) * 16 + (lane & 15);
+    if (m >= rows) continue;
+#pragma unroll
+    for (int a = 0; a < C::kTu / 2; ++a) {
+      const int c = (wu * C::kTu + 2 * a) * 16 + (lane >> 4) * 8;
+      float o[8];
+      prod.eight(o, a, v);
+      if (c < cols) store8(out + (size_t)m * ld + c, o);
     }
   }
 }
@@ -389,7 +456,6 @@ grad_x_kernel(MatmulGradParams p, const uint16_t* gz, int ntiles) {
   Tile t;
   if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = lane_id();
   const int n0 = t.n * C::kBu;
   const uint32_t lda = (uint32_t)p.K * 2, ldb = (uint32_t)p.P * 2;
   Product prod;
@@ -400,19 +466,7 @@ grad_x_kernel(MatmulGradParams p, const uint16_t* gz, int ntiles) {
   for (int i = 0; i < Product::A::kLoads; ++i)
     ap[i] = reinterpret_cast<const char*>(p.weight + (size_t)t.e * p.P * p.K + n0);
   prod.run(smem, wave, ap, reinterpret_cast<const char*>(gz) + (size_t)t.m0 * ldb, lda, ldb, p.P);
-  const int wu = wave % C::kWu, wv = wave / C::kWu;
-#pragma unroll
-  for (int v = 0; v < C::kTv; ++v) {
-    const int m = t.m0 + (wv * C::kTv + v) * 16 + (lane & 15);
-    if (m >= t.end) continue;
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u) {
-      const int c = n0 + (wu * C::kTu + u) * 16 + (lane >> 4) * 4;
-      const float o[4] = {prod.acc[u][v][0], prod.acc[u][v][1], prod.acc[u][v][2],
-                          prod.acc[u][v][3]};
-      if (c < p.K) store4(p.grad_x + (size_t)m * p.K + c, o);
-    }
-  }
+  store_tile<C>(prod, wave, p.grad_x + (size_t)t.m0 * p.K + n0, p.K, t.end - t.m0, p.K - n0);
 }
 
 // grad_w: D[input feature][weight row], summed over the expert's rows.
@@ -428,7 +482,6 @@ grad_w_kernel(MatmulGradParams p, const uint16_t* gz, unsigned nt, unsigned pt) 
   int begin, end;
   segment_of(p.seg, e, begin, end);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = lane_id();
   const uint32_t lda = (uint32_t)p.K * 2, ldb = (uint32_t)p.P * 2;
   Product prod;
   if (end > begin) {
@@ -441,30 +494,16 @@ grad_w_kernel(MatmulGradParams p, const uint16_t* gz, unsigned nt, unsigned pt) 
     prod.run(smem, wave, ap, reinterpret_cast<const char*>(gz + (size_t)begin * p.P + p0), lda,
              ldb, end - begin);
   } else {
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u)
-#pragma unroll
-      for (int v = 0; v < C::kTv; ++v) prod.acc[u][v] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    prod.clear();
   }
-  const int wu = wave % C::kWu, wv = wave / C::kWu;
-#pragma unroll
-  for (int v = 0; v < C::kTv; ++v) {
-    const int row = p0 + (wv * C::kTv + v) * 16 + (lane & 15);
-    if (row >= p.P) continue;
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u) {
-      const int c = n0 + (wu * C::kTu + u) * 16 + (lane >> 4) * 4;
-      const float o[4] = {prod.acc[u][v][0], prod.acc[u][v][1], prod.acc[u][v][2],
-                          prod.acc[u][v][3]};
-      if (c < p.K) store4(p.grad_weight + ((size_t)e * p.P + row) * p.K + c, o);
-    }
-  }
+  store_tile<C>(prod, wave, p.grad_weight + ((size_t)e * p.P + p0) * p.K + n0, p.K, p.P - p0,
+                p.K - n0);
 }
 
 // 256 x 256 tiles for experts of many rows, 256 x 128 for those of few: a part
 // tile wastes the products of its missing rows.
-using Large = Config<2, 4, 8, 4>;
-using Small = Config<4, 2, 4, 4>;
+using Large = Config<2, 2, 8, 8>;
+using Small = Config<2, 2, 8, 4>;
 
 // Large tiles where an expert has more rows than one small tile on average
 // and the large tiles alone fill the 256 compute units.
@@ -482,7 +521,7 @@ hipError_t allow_lds(K kernel, int bytes) {
 template <class C, int ACT>
 hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
   constexpr int kCols = ACT == kActSwiglu ? C::kBu / 2 : C::kBu;
-  constexpr int kLds = 2 * TileProduct<C, false, false>::kStage;
+  constexpr int kLds = TileProduct<C, false, false>::kLds;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
@@ -507,7 +546,7 @@ hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
 
 template <class C>
 hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStream_t st) {
-  constexpr int kLds = 2 * TileProduct<C, true, false>::kStage;
+  constexpr int kLds = TileProduct<C, true, false>::kLds;
   const int ntiles = (p.K + C::kBu - 1) / C::kBu;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
@@ -520,7 +559,7 @@ hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStrea
 
 template <class C>
 hipError_t launch_grad_w(const MatmulGradParams& p, const uint16_t* gz, hipStream_t st) {
-  constexpr int kLds = 2 * TileProduct<C, true, true>::kStage;
+  constexpr int kLds = TileProduct<C, true, true>::kLds;
   const unsigned nt = (p.K + C::kBu - 1) / C::kBu, pt = (p.P + C::kBv - 1) / C::kBv;
   const int64_t grid = (int64_t)nt * pt * p.seg.E;
   if (grid > INT32_MAX) return hipErrorInvalidValue;

@@ -86,6 +86,18 @@ __device__ __forceinline__ void wait_vm() {
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// c += a b on the 16 x 16 x 32 matrix unit, the accumulators staying where they
+// are: with the builtin the compiler moved them between registers around the
+// loops over a tile (as many moves as products at 256 accumulators).  The
+// compiler does not see that this is a matrix instruction: after the last one
+// mfma_results, then mfma_result on every accumulator, before it is read.
+__device__ __forceinline__ void mfma_in_place(f32x4_t& c, bf16x8_t a, bf16x8_t b) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+// The last product's results get written (8 passes of 4 cycles).
+__device__ __forceinline__ void mfma_results() { asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15"); }
+__device__ __forceinline__ void mfma_result(f32x4_t& c) { asm volatile("" : "+a"(c)); }
+
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)reinterpret_cast<const __attribute__((address_space(3))) void*>(
       (uintptr_t)p);
@@ -98,102 +110,115 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // through the transposing LDS load.  Both are filled by wave loads of 1 KB, so
 // the layout is linear in the lanes and the 16-byte chunks of a row are
 // permuted on the global side instead: chunk c of row i sits in slot c ^ f(i),
-// which spreads the reads of a fragment over all banks.
+// which spreads the reads of a fragment over all banks (no conflicts counted).
 // ---------------------------------------------------------------------------
 constexpr int kStep = 64;
+constexpr int kPart = 32;             // r values of one 16 x 16 x 32 product
+constexpr int kParts = kStep / kPart;
 
-template <int SIZE, int WAVES, bool TRANSPOSED>
+// PAIRED, for the operand that makes the output's contiguous dimension: two
+// neighbouring fragments share 32 rows, row g * 8 + b * 4 + i being row
+// g * 4 + i of fragment b, so that the pair leaves every lane with 8
+// neighbouring outputs.
+template <int SIZE, int WAVES, bool TRANSPOSED, bool PAIRED>
 struct OperandTile {
   static constexpr int kBytes = SIZE * kStep * 2;
   static constexpr int kLoads = kBytes / 1024 / WAVES;  // wave loads per wave and step
   static_assert(kLoads * WAVES * 1024 == kBytes, "whole wave loads");
-  uint32_t off[kLoads];   // byte offset of this lane's chunk, step 0
-  uint16_t where[kLoads]; // its first position along r within a step
+  static constexpr int kSlots = TRANSPOSED ? SIZE / 8 : kStep / 8;  // chunks in a row
+  static constexpr int kRowsPerLoad = 64 / kSlots;
+  uint32_t off[kLoads];    // byte offset of this lane's chunk, step 0
+  uint16_t where[kLoads];  // its first position along r within a step
 
   static __device__ __forceinline__ int swizzle(int row) {
-    return TRANSPOSED ? ((row & 3) | ((row >> 3) & 1) << 2) << 1 : (row >> 1) & 7;
+    if (TRANSPOSED) return ((row & 3) | ((row >> 3) & 1) << 2) << 1;
+    return PAIRED ? ((row >> 1) & 1) | ((row >> 3) & 3) << 1 : (row >> 1) & 7;
+  }
+  // The chunk that this lane brings in with load q of the tile, and its row.
+  static __device__ __forceinline__ void chunk_of(int q, int& row, int& c) {
+    const int lane = lane_id();
+    row = q * kRowsPerLoad + lane / kSlots;
+    c = (lane % kSlots) ^ swizzle(row);
   }
 
   // ld: bytes between rows.  valid: rows (columns, when transposed: a multiple
   // of 8) the tile really has, at least one (eight); past them the last one is
   // read again.
   __device__ __forceinline__ void init(int wave, uint32_t ld, int valid) {
-    const int lane = lane_id();
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int q = wave * kLoads + i;
+      int row, c;
+      chunk_of(wave * kLoads + i, row, c);
       if constexpr (TRANSPOSED) {
-        constexpr int kSlots = SIZE / 8;  // chunks in a row
-        const int at = q * 64 + lane;
-        const int r = at / kSlots;
-        const int c = min(((at % kSlots) ^ swizzle(r)) * 8, valid - 8);
-        off[i] = (uint32_t)r * ld + (uint32_t)c * 2;
-        where[i] = (uint16_t)r;
+        off[i] = (uint32_t)row * ld + (uint32_t)min(c * 8, valid - 8) * 2;
+        where[i] = (uint16_t)row;
       } else {
-        const int row = q * 8 + lane / 8;
-        const int c = (lane % 8) ^ swizzle(row);
         off[i] = (uint32_t)min(row, valid - 1) * ld + (uint32_t)c * 16;
         where[i] = (uint16_t)(c * 8);
       }
     }
   }
-  // Start the loads of one step: base[i] is where load i starts in it.
+  // Start load i of a step whose first value, for this load, is at base.
   // left < kStep: only that many positions exist, others re-read the first.
   template <bool TAIL>
-  __device__ __forceinline__ void load(uint32_t lds, int wave, const char* const (&base)[kLoads],
+  __device__ __forceinline__ void load(int i, uint32_t lds, int wave, const char* base,
                                        uint32_t ld, int left) const {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      uint32_t o = off[i];
-      if (TAIL && (int)where[i] >= left)
-        o -= TRANSPOSED ? (uint32_t)where[i] * ld : (uint32_t)where[i] * 2;
-      load_to_lds(lds + (uint32_t)(wave * kLoads + i) * 1024, base[i], o);
-    }
+    uint32_t o = off[i];
+    if (TAIL && (int)where[i] >= left)
+      o -= TRANSPOSED ? (uint32_t)where[i] * ld : (uint32_t)where[i] * 2;
+    load_to_lds(lds + (uint32_t)(wave * kLoads + i) * 1024, base, o);
   }
+
   // Reading fragments: N of 16 rows each (columns, when transposed) from i0
-  // on.  Lane l of fragment n holds row l & 15 and, of the 32 values along r
-  // from ks * 32 on, (l >> 4) * 8 .. + 7.  The swizzle depends on the lane
-  // alone (and, transposed, on n), so the addresses are made once and the rest
-  // is in the instructions' offsets.
+  // on.  Lane l of a fragment holds its row l & 15 and, of part k of the step,
+  // the positions (l >> 4) * 8 .. + 7.  The swizzle depends on the lane alone
+  // (and on k, or on n when transposed), so the addresses are made once and
+  // the rest is in the instructions' offsets.
   template <int N>
   struct Reader {
-    uint32_t at[TRANSPOSED ? N : kStep / 32];
+    static constexpr int kAts = !TRANSPOSED ? kParts : PAIRED ? N / 2 : N;
+    uint32_t at[kAts];
     __device__ __forceinline__ void init(int i0) {
-      const int lane = lane_id();
+      const int lane = lane_id(), j = lane & 15;
       if constexpr (TRANSPOSED) {
-        const int row = (lane >> 4) * 8 + ((lane & 15) >> 2);
+        // 16 lanes turn a block of 4 positions x 16 columns around: lane j of
+        // them names 8 bytes of it and receives column j
+        const int row = (lane >> 4) * 8 + (j >> 2);
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-          at[n] = (uint32_t)(row * (SIZE * 2) + ((i0 / 8 + 2 * n) ^ swizzle(row)) * 16 +
-                             (lane & 3) * 8);
+        for (int n = 0; n < kAts; ++n) {
+          const int col = i0 + (PAIRED ? n * 32 + (j & 3) * 8 : n * 16 + (j & 3) * 4);
+          at[n] = (uint32_t)(row * (SIZE * 2) + ((col / 8) ^ swizzle(row)) * 16 + (col & 4) * 2);
+        }
       } else {
-        const int row = i0 + (lane & 15);
+        const int row = i0 + (PAIRED ? (j >> 2) * 8 + (j & 3) : j);
 #pragma unroll
-        for (int ks = 0; ks < kStep / 32; ++ks)
-          at[ks] = (uint32_t)(row * (kStep * 2) + ((ks * 4 + (lane >> 4)) ^ swizzle(row)) * 16);
+        for (int k = 0; k < kParts; ++k)
+          at[k] = (uint32_t)(row * (kStep * 2) + ((k * 4 + (lane >> 4)) ^ swizzle(row)) * 16);
       }
     }
-    // lds: LDS address of the operand's step.  TAIL: values at or past left
+    // lds: LDS address of the operand's step.  TAIL: positions at or past left
     // are zero.
     template <bool TAIL>
-    __device__ __forceinline__ bf16x8_t frag(uint32_t lds, int n, int ks, int left) const {
+    __device__ __forceinline__ bf16x8_t frag(uint32_t lds, int n, int k, int left) const {
       union {
         bf16x8_t v;
         i16x4_t h[2];
         uint32_t w[4];
       } u;
       if constexpr (TRANSPOSED) {
+        const uint32_t p = lds + (PAIRED ? at[n / 2] + n % 2 * 8 : at[n]);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
               (__attribute__((address_space(3))) i16x4_t*)(uintptr_t)(
-                  lds + at[n] + (ks * 32 + h * 4) * (SIZE * 2)));
+                  p + (k * kPart + h * 4) * (SIZE * 2)));
       } else {
+        const int row = PAIRED ? n / 2 * 32 + n % 2 * 4 : n * 16;
         u.v = *(const __attribute__((address_space(3))) bf16x8_t*)(uintptr_t)(
-            lds + at[ks] + n * 16 * (kStep * 2));
+            lds + at[k] + row * (kStep * 2));
       }
       if constexpr (TAIL) {
-        const int r = ks * 32 + (lane_id() >> 4) * 8;
+        const int r = k * kPart + (lane_id() >> 4) * 8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t lo = r + 2 * j < left ? 0x0000ffffu : 0u;
