@@ -8,6 +8,7 @@ namespace moe {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActSwiglu = 3 };
 

@@ -24,19 +24,14 @@ namespace moe {
 
 namespace {
 
-constexpr int kTile = 64;   // fp8: tile and step of the product over widened codes
-constexpr int kCodes = 32;
-constexpr int kPitch = kCodes + 8;
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
 
 // ---------------------------------------------------------------------------
 // The tile product
 // ---------------------------------------------------------------------------
-// WU x WV waves of TU x TV fragments of 16 x 16.
+// WU x WV waves of TU x TV fragments of 16 x 16.  A wave's fragments lie side
+// by side along u and kWv apart along v, so that the rows of a part tile are
+// spread over all waves.
 template <int WU, int WV, int TU, int TV>
 struct Config {
   static constexpr int kWu = WU, kWv = WV, kTu = TU, kTv = TV;
@@ -64,7 +59,7 @@ struct TileProduct {
   template <bool TAIL>
   __device__ __forceinline__ void read(Fragments& f, int i, uint32_t lds, int k, int left) const {
     if (i < C::kTv)
-      f.b[i] = rb.template frag<TAIL>(lds + A::kBytes, i, k, left);
+      f.b[i] = rb.template frag<TAIL>(lds + A::kBytes, i * (BT ? 1 : C::kWv), k, left);
     else
       f.a[i - C::kTv] = ra.template frag<TAIL>(lds, i - C::kTv, k, left);
   }
@@ -103,7 +98,7 @@ struct TileProduct {
                                       const char* bp, uint32_t lda, uint32_t ldb, int red) {
     static_assert(kParts == 2, "the parts are written out");
     ra.init(wave % C::kWu * C::kTu * 16);
-    rb.init(wave / C::kWu * C::kTv * 16);
+    rb.init(wave / C::kWu * 16, C::kWv);
     clear();
     const size_t sta = AT ? (size_t)kStep * lda : (size_t)kStep * 2;
     const size_t stb = BT ? (size_t)kStep * ldb : (size_t)kStep * 2;
@@ -205,114 +200,134 @@ struct TileProduct {
   }
 
   // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours
-  // along u from a * 32 + (lane >> 4) * 8 on, of row v * 16 + (lane & 15).
+  // along u from a * 32 + (lane >> 4) * 8 on, of the fragment's row lane & 15.
   __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
   }
 };
 
-// e4m3 codes widened to bf16 (exact).
-__device__ __forceinline__ void stage_codes(uint16_t (*s)[kPitch], const uint8_t* m, size_t ld,
-                                            const int row, bool in, int r0) {
-  const int i = threadIdx.x / 4, c = (threadIdx.x % 4) * 8;
-  uint2 v = make_uint2(0, 0);
-  if (in) v = *reinterpret_cast<const uint2*>(m + (size_t)row * ld + r0 + c);
-  float f[8];
-  e4m3x4_to_f32(v.x, f);
-  e4m3x4_to_f32(v.y, f + 4);
-#pragma unroll
-  for (int e = 0; e < 8; e += 2)
-    *reinterpret_cast<uint32_t*>(&s[i][c + e]) = pack_bf16x2(f[e], f[e + 1]);
-}
+// ---------------------------------------------------------------------------
+// The same for e4m3 operands with a scale per 128 values along r: one step is
+// one block of 128, whose products are summed by one 16 x 16 x 128 matrix
+// instruction per fragment and then scaled in fp32, sx of the token times sw
+// of the 128 weight rows.  A row of a step is 128 bytes, as in the bf16
+// product, so the tiles in LDS are the same; the chunks of a fragment are
+// taken in an order of their own, equal for both operands, which a sum does
+// not notice.  Eight waves, and three steps in LDS: a serving batch has few
+// rows an expert, so the weights stream through once and the loads in flight
+// count.
+// ---------------------------------------------------------------------------
+template <class C>
+struct Fp8Product {
+  using A = OperandTile<C::kBu, C::kWaves, false, true>;
+  using B = OperandTile<C::kBv, C::kWaves, false, false>;
+  static constexpr int kScales = C::kWaves * 256;  // one dword a lane
+  static_assert(C::kBv == C::kWaves * 32, "a wave brings in the scales of 32 rows");
+  static constexpr int kStage = A::kBytes + B::kBytes + kScales;
+  static constexpr int kStages = 3, kLds = kStages * kStage;
+  static constexpr int kLoads = A::kLoads + B::kLoads + 1;
+  A a;
+  B b;
+  f32x4_t acc[C::kTu][C::kTv];
+  typename A::template Reader<C::kTu> ra;
+  typename B::template Reader<C::kTv> rb;
 
-__device__ __forceinline__ bf16x8_t frag(uint16_t (*s)[kPitch], int i0) {
-  const int lane = lane_id();
-  return *reinterpret_cast<const bf16x8_t*>(&s[i0 + (lane & 15)][(lane >> 4) * 8]);
-}
+  template <class R>
+  static __device__ __forceinline__ i32x8_t frag(const R& r, uint32_t lds, int n) {
+    union {
+      bf16x8_t h[2];
+      i32x8_t v;
+    } u;
+    u.h[0] = r.template frag<false>(lds, n, 0, 0);
+    u.h[1] = r.template frag<false>(lds, n, 1, 0);
+    return u.v;
+  }
 
-__device__ __forceinline__ void mma_step(f32x4_t (&acc)[4], uint16_t (*sa)[kPitch],
-                                         uint16_t (*sb)[kPitch]) {
-  const bf16x8_t b = frag(sb, (threadIdx.x / kWave) * 16);
+  // blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
+  // 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of the weight rows
+  // behind the first and the second half of the wave's fragments.  (A plain
+  // load of them would wait for every load to LDS before it.)  rows: how many
+  // the tile has.
+  __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
+                                      const char* bp, const float* scale, int blocks, int rows) {
+    ra.init(wave % C::kWu * C::kTu * 16);
+    rb.init(wave / C::kWu * 16);
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-    acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sa, u * 16), b, acc[u], 0, 0, 0);
-}
-
-template <int ACT>
-__global__ void __launch_bounds__(kThreads)
-matmul_fp8_kernel(MatmulParams p) {
-  __shared__ __align__(16) uint16_t sa[kTile][kPitch], sb[kTile][kPitch];
-  constexpr bool kGated = ACT == kActSwiglu;
-  constexpr int kCols = kGated ? kTile / 2 : kTile;  // output columns of a block
-  const int e = blockIdx.y;
-  const int n0 = blockIdx.x * kCols;
-  int begin, end;
-  segment_of(p.seg, e, begin, end);
-  const int lane = lane_id();
-  const int srow = threadIdx.x / 4;  // the tile row this thread stages
-  // the weight row behind tile row srow (gate rows, then up rows), or -1
-  const int col = n0 + (kGated ? srow % kCols : srow);
-  const int wrow = col < p.F ? (kGated && srow >= kCols ? p.F + col : col) : -1;
-  for (int m0 = begin; m0 < end; m0 += kTile) {
-    const int m = m0 + (threadIdx.x / kWave) * 16 + (lane & 15);
-    f32x4_t acc[4] = {};
-    const uint8_t* w = static_cast<const uint8_t*>(p.weight) + (size_t)e * p.P * p.K;
-    const uint8_t* x = static_cast<const uint8_t*>(p.x);
-    const int kb = p.K / 128;
-    for (int b = 0; b < kb; ++b) {
-      f32x4_t part[4] = {};
-      for (int r0 = b * 128; r0 < b * 128 + 128; r0 += kCodes) {
-        __syncthreads();
-        stage_codes(sa, w, p.K, max(wrow, 0), wrow >= 0, r0);
-        stage_codes(sb, x, p.K, min(m0 + srow, end - 1), m0 + srow < end, r0);
-        __syncthreads();
-        mma_step(part, sa, sb);
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
+    const uint32_t lds = lds_address(smem), lds_end = lds + kLds;
+    uint32_t fill = lds, here = lds;
+    auto after = [&](uint32_t slot) { return slot + kStage == lds_end ? lds : slot + kStage; };
+    auto start = [&] {
+#pragma unroll
+      for (int i = 0; i < A::kLoads; ++i) {
+        a.template load<false>(i, fill, wave, ap[i], 0, 0);
+        ap[i] += 128;
       }
-      const float sx = m < end ? p.x_scales[(size_t)m * kb + b] : 0.0f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = n0 + (kGated ? (u % 2) * 16 : u * 16) + (lane >> 4) * 4;
-        const int row = min(c, p.F - 1) + (kGated && u >= 2 ? p.F : 0);
-        const float s =
-            sx * p.weight_scales[((size_t)e * (p.P / 128) + row / 128) * kb + b];
+      for (int i = 0; i < B::kLoads; ++i)
+        b.template load<false>(i, fill + A::kBytes, wave, bp, 0, 0);
+      load4_to_lds(fill + A::kBytes + B::kBytes + wave * 256, scale);
+      bp += 128;
+      scale += 1;
+      fill = after(fill);
+    };
+    start();
+    if (blocks > 1) start();
+    // the fragments of this wave that hold rows at all
+    const int wv = wave / C::kWu;
+    const int nv = min((rows - wv * 16 + C::kWv * 16 - 1) / (C::kWv * 16), C::kTv);
+    // 32 rows of scales every 256 bytes, this wave's two behind its own 32
+    const uint32_t scales = A::kBytes + B::kBytes;
+    const uint32_t sw_at = scales + wave * 256 + 128;
+    const uint32_t sx_at = scales + wv / 2 * 256 + wv % 2 * 64 + (lane_id() & 15) * 4;
+    static_assert(C::kWv % 2 == 0, "a fragment's scales lie 256 bytes per two fragments on");
+    auto lds_float = [](uint32_t p) {
+      return *(const __attribute__((address_space(3))) float*)(uintptr_t)p;
+    };
+    for (int t = 0; t < blocks; ++t) {
+      if (t + 1 < blocks)
+        wait_vm<kLoads>();
+      else
+        wait_vm<0>();
+      wait_lds();  // this wave has read the step before out
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (t + 2 < blocks) start();
+      if (nv > 0) {
+        const float sw[2] = {lds_float(here + sw_at), lds_float(here + sw_at + 4)};
+        i32x8_t fa[C::kTu];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[u][i] = fmaf(part[u][i], s, acc[u][i]);
+        for (int u = 0; u < C::kTu; ++u) fa[u] = frag(ra, here, u);
+#pragma unroll
+        for (int v = 0; v < C::kTv; ++v) {
+          if (v >= nv) break;
+          const i32x8_t fb = frag(rb, here + A::kBytes, v * C::kWv);
+          const float sx = lds_float(here + sx_at + v * C::kWv / 2 * 256);
+          f32x4_t part[C::kTu];
+#pragma unroll
+          for (int u = 0; u < C::kTu; ++u)
+            part[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[u], fb, f32x4_t{}, 0, 0,
+                                                                       0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < C::kTu; ++u) {
+            const float s = sx * sw[u < C::kTu / 2 ? 0 : 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[u][v][i] = fmaf(part[u][i], s, acc[u][v][i]);
+          }
+        }
       }
-    }
-    if (m >= end) continue;
-    float z[4][4];
-    int cols[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      cols[u] = n0 + (kGated ? (u % 2) * 16 : u * 16) + (lane >> 4) * 4;
-      const int row = cols[u] + (kGated && u >= 2 ? p.F : 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[u][i] = acc[u][i];
-        if (p.bias && cols[u] < p.F) z[u][i] += p.bias[(size_t)e * p.P + row + i];
-      }
-      if (p.pre && cols[u] < p.F) store4(p.pre + (size_t)m * p.P + row, z[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < (kGated ? 2 : 4); ++u) {
-      if (cols[u] >= p.F) continue;
-      float o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (kGated)
-          o[i] = z[u][i] * sigmoid_f32(z[u][i]) * z[u + 2][i];
-        else
-          o[i] = act_f32<ACT>(z[u][i]);
-      }
-      const size_t at = (size_t)m * p.F + cols[u];
-      if (p.residual)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += bf16_f32(p.residual[at + i]);
-      store4(p.y + at, o);
+      here = after(here);
     }
   }
-}
+
+  __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
+  }
+};
 
 // gz = grad_y * act'(pre) to bf16, and its column sums in fp32: a thread owns
 // one column and the block walks the expert's rows.
@@ -360,71 +375,119 @@ act_grad_kernel(MatmulGradParams p, uint16_t* gz) {
 // y (and pre): u runs over weight rows; a gated layer's wave takes half of its
 // fragments from the gate rows and half from the up rows of the same columns.
 template <class C, int ACT>
-__global__ void __launch_bounds__(C::kThreads)
-matmul_kernel(MatmulParams p, int ntiles) {
-  using Product = TileProduct<C, false, false>;
-  using A = typename Product::A;
-  constexpr bool kGated = ACT == kActSwiglu;
-  constexpr int kPairs = (kGated ? C::kTu / 2 : C::kTu) / 2;  // along the output's columns
-  constexpr int kWaveCols = kPairs * 32;                // output columns of a wave
-  constexpr int kCols = kWaveCols * C::kWu;          // and of the tile
-  extern __shared__ __align__(1024) char smem[];
-  Tile t;
-  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = lane_id();
-  const int n0 = t.n * kCols;
-  const uint32_t ld = (uint32_t)p.K * 2;
-  const char* w = static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld;
-  Product prod;
-  const char* ap[A::kLoads];
+struct Columns {
+  static constexpr bool kGated = ACT == kActSwiglu;
+  static constexpr int kPairs = (kGated ? C::kTu / 2 : C::kTu) / 2;  // along the output's columns
+  static constexpr int kWave = kPairs * 32;                          // output columns of a wave
+  static constexpr int kTile = kWave * C::kWu;                       // and of the tile
+};
+
+// This wave's loads of weight rows: w is the first of the tile's (gate) rows,
+// cols how many columns are left from there, ld the bytes of a row.
+template <class C, int ACT, class A>
+__device__ __forceinline__ void weight_loads(A& a, const char* (&ap)[A::kLoads], const char* w,
+                                             int wave, int F, int cols, uint32_t ld) {
+  using Cols = Columns<C, ACT>;
 #pragma unroll
   for (int i = 0; i < A::kLoads; ++i) {
-    // the weight row behind tile row `row`: a gated wave's first rows are gate
-    // rows, the others the up rows of the same columns
     const int q = wave * A::kLoads + i;
     int row, c;
     A::chunk_of(q, row, c);
     const int first = q * A::kRowsPerLoad;  // the load's rows are of one kind
-    const bool up = kGated && first % (2 * kWaveCols) >= kWaveCols;
+    const bool up = Cols::kGated && first % (2 * Cols::kWave) >= Cols::kWave;
     const int col =
-        kGated ? row / (2 * kWaveCols) * kWaveCols + row % kWaveCols : row;
-    prod.a.off[i] = (uint32_t)min(col, p.F - 1 - n0) * ld + (uint32_t)c * 16;
-    prod.a.where[i] = (uint16_t)(c * 8);
-    ap[i] = w + (up ? (size_t)p.F * ld : 0);
+        Cols::kGated ? row / (2 * Cols::kWave) * Cols::kWave + row % Cols::kWave : row;
+    a.off[i] = (uint32_t)min(col, cols - 1) * ld + (uint32_t)c * 16;
+    a.where[i] = (uint16_t)(c * 8);
+    ap[i] = w + (up ? (size_t)F * ld : 0);
   }
-  prod.b.init(wave, ld, min(C::kBv, t.end - t.m0));
-  prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, ld, ld, p.K);
+}
 
-  const int wu = wave % C::kWu, wv = wave / C::kWu;
+// Bias, activation and residual on the accumulators, then the one rounding.
+template <class C, int ACT, class Product>
+__device__ __forceinline__ void finish(const Product& prod, const MatmulParams& p, const Tile& t,
+                                       int wave) {
+  using Cols = Columns<C, ACT>;
+  const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
 #pragma unroll
   for (int v = 0; v < C::kTv; ++v) {
-    const int m = t.m0 + (wv * C::kTv + v) * 16 + (lane & 15);
+    const int m = t.m0 + (v * C::kWv + wv) * 16 + (lane & 15);
     if (m >= t.end) continue;
 #pragma unroll
-    for (int a = 0; a < kPairs; ++a) {
-      const int col = n0 + wu * kWaveCols + a * 32 + (lane >> 4) * 8;
+    for (int a = 0; a < Cols::kPairs; ++a) {
+      const int col = t.n * Cols::kTile + wu * Cols::kWave + a * 32 + (lane >> 4) * 8;
       if (col >= p.F) continue;
       float z[8], up[8];
       prod.eight(z, a, v);
-      if (kGated) prod.eight(up, a + kPairs, v);
+      if (Cols::kGated) prod.eight(up, a + Cols::kPairs, v);
       if (p.bias) {
         const float* b = p.bias + (size_t)t.e * p.P + col;
         add8(z, b);
-        if (kGated) add8(up, b + p.F);
+        if (Cols::kGated) add8(up, b + p.F);
       }
       if (p.pre) {
         store8(p.pre + (size_t)m * p.P + col, z);
-        if (kGated) store8(p.pre + (size_t)m * p.P + p.F + col, up);
+        if (Cols::kGated) store8(p.pre + (size_t)m * p.P + p.F + col, up);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        z[i] = kGated ? z[i] * sigmoid_f32(z[i]) * up[i] : act_f32<ACT>(z[i]);
+        z[i] = Cols::kGated ? z[i] * sigmoid_f32(z[i]) * up[i] : act_f32<ACT>(z[i]);
       const size_t at = (size_t)m * p.F + col;
       if (p.residual) add8(z, p.residual + at);
       store8(p.y + at, z);
     }
   }
+}
+
+template <class C, int ACT>
+__global__ void __launch_bounds__(C::kThreads)
+matmul_kernel(MatmulParams p, int ntiles) {
+  using Product = TileProduct<C, false, false>;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n0 = t.n * Columns<C, ACT>::kTile;
+  const uint32_t ld = (uint32_t)p.K * 2;
+  Product prod;
+  const char* ap[Product::A::kLoads];
+  weight_loads<C, ACT>(prod.a, ap,
+                       static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld, wave,
+                       p.F, p.F - n0, ld);
+  prod.b.init(wave, ld, min(C::kBv, t.end - t.m0));
+  prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, ld, ld, p.K);
+  finish<C, ACT>(prod, p, t, wave);
+}
+
+template <class C, int ACT>
+__global__ void __launch_bounds__(C::kThreads)
+matmul_fp8_kernel(MatmulParams p, int ntiles) {
+  using Product = Fp8Product<C>;
+  using Cols = Columns<C, ACT>;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n0 = t.n * Cols::kTile, kb = p.K / 128;
+  const uint32_t ld = (uint32_t)p.K;
+  const int rows = min(C::kBv, t.end - t.m0);
+  Product prod;
+  const char* ap[Product::A::kLoads];
+  weight_loads<C, ACT>(prod.a, ap,
+                       static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld, wave,
+                       p.F, p.F - n0, ld);
+  prod.b.init(wave, ld, rows);
+  // the scales of this wave's weight rows (all of one block of 128, or of the
+  // gate's and the up's block); past the last column any will do
+  static_assert(128 % Cols::kWave == 0, "a wave's columns lie in one block of scales");
+  const int block = min(n0 + wave % C::kWu * Cols::kWave, p.F - 1) / 128;
+  const int lane = lane_id();
+  const size_t up = Cols::kGated && lane % 2 == 1 ? p.F / 128 : 0;
+  const float* scale =
+      lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
+                : p.weight_scales + ((size_t)t.e * (p.P / 128) + block + up) * kb;
+  prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, scale, kb, rows);
+  finish<C, ACT>(prod, p, t, wave);
 }
 
 // The accumulators as bf16 rows: row v of the tile to out + v * ld, for v
@@ -435,7 +498,7 @@ __device__ __forceinline__ void store_tile(const Product& prod, int wave, uint16
   const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
 #pragma unroll
   for (int v = 0; v < C::kTv; ++v) {
-    const int m = (wv * C::kTv + v) * 16 + (lane & 15);
+    const int m = (v * C::kWv + wv) * 16 + (lane & 15);
     if (m >= rows) continue;
 #pragma unroll
     for (int a = 0; a < C::kTu / 2; ++a) {
@@ -507,6 +570,10 @@ using Small = Config<2, 2, 8, 4>;
 
 // Large tiles where an expert has more rows than one small tile on average
 // and the large tiles alone fill the 256 compute units.
+// fp8: 128 weight rows by 256 token rows, so that an expert's weights are read
+// once however its 128 or so rows fall.
+using Codes = Config<2, 4, 4, 4>;
+
 bool large_tiles(const Segments& s, int u) {
   const int64_t tiles = ((int64_t)s.pairs / Large::kBv) * ((u + Large::kBu - 1) / Large::kBu);
   return s.pairs / s.E > Small::kBv && tiles >= 256;
@@ -518,30 +585,26 @@ hipError_t allow_lds(K kernel, int bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <class C, int ACT>
-hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
-  constexpr int kCols = ACT == kActSwiglu ? C::kBu / 2 : C::kBu;
-  constexpr int kLds = TileProduct<C, false, false>::kLds;
+template <class C, int ACT, class Product, class Kernel>
+hipError_t launch_tiles(Kernel kernel, const MatmulParams& p, hipStream_t st) {
+  constexpr int kCols = Columns<C, ACT>::kTile;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds(matmul_kernel<C, ACT>, kLds);
+  const hipError_t e = allow_lds(kernel, Product::kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((matmul_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p,
-                     ntiles);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(C::kThreads), Product::kLds, st, p, ntiles);
   return hipGetLastError();
 }
 
 template <int ACT>
 hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
-  if (fp8) {
-    const int cols = ACT == kActSwiglu ? kTile / 2 : kTile;
-    hipLaunchKernelGGL((matmul_fp8_kernel<ACT>), dim3((p.F + cols - 1) / cols, p.seg.E),
-                       dim3(kThreads), 0, st, p);
-    return hipGetLastError();
-  }
-  if (large_tiles(p.seg, p.P)) return launch_tiles<Large, ACT>(p, st);
-  return launch_tiles<Small, ACT>(p, st);
+  if (fp8) return launch_tiles<Codes, ACT, Fp8Product<Codes>>(matmul_fp8_kernel<Codes, ACT>, p, st);
+  if (large_tiles(p.seg, p.P))
+    return launch_tiles<Large, ACT, TileProduct<Large, false, false>>(matmul_kernel<Large, ACT>, p,
+                                                                      st);
+  return launch_tiles<Small, ACT, TileProduct<Small, false, false>>(matmul_kernel<Small, ACT>, p,
+                                                                    st);
 }
 
 template <class C>

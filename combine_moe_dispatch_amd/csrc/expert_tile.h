@@ -80,6 +80,13 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const void* base, uint
                : "s"(lds), "v"(offset), "s"(base)
                : "memory");
 }
+// 4 bytes a lane from an address of its own, lane i at lds + 4 i.
+__device__ __forceinline__ void load4_to_lds(uint32_t lds, const void* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -178,7 +185,9 @@ struct OperandTile {
   struct Reader {
     static constexpr int kAts = !TRANSPOSED ? kParts : PAIRED ? N / 2 : N;
     uint32_t at[kAts];
-    __device__ __forceinline__ void init(int i0) {
+    // apart: fragments of the operand between two of this reader's (transposed
+    // only; else the caller numbers them so)
+    __device__ __forceinline__ void init(int i0, int apart = 1) {
       const int lane = lane_id(), j = lane & 15;
       if constexpr (TRANSPOSED) {
         // 16 lanes turn a block of 4 positions x 16 columns around: lane j of
@@ -186,7 +195,7 @@ struct OperandTile {
         const int row = (lane >> 4) * 8 + (j >> 2);
 #pragma unroll
         for (int n = 0; n < kAts; ++n) {
-          const int col = i0 + (PAIRED ? n * 32 + (j & 3) * 8 : n * 16 + (j & 3) * 4);
+          const int col = i0 + (PAIRED ? n * 32 + (j & 3) * 8 : n * apart * 16 + (j & 3) * 4);
           at[n] = (uint32_t)(row * (SIZE * 2) + ((col / 8) ^ swizzle(row)) * 16 + (col & 4) * 2);
         }
       } else {
