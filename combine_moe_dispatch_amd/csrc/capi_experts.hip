@@ -115,7 +115,8 @@ moe_status moe_expert_matmul_backward(const moe_shape* shape, const moe_linear* 
   if (st != MOE_OK) return st;
   if ((st = check_linear(shape, linear, &p.P)) != MOE_OK) return st;
   if (shape->payload != MOE_PAYLOAD_BF16) return MOE_ERR_UNSUPPORTED;
-  const size_t need = moe_expert_matmul_backward_workspace_size(shape, linear);
+  const bool idle = linear->activation == MOE_ACT_NONE && !grad_bias;  // gz is grad_y
+  const size_t need = idle ? 0 : moe_expert_matmul_backward_workspace_size(shape, linear);
   if ((st = segments(shape, layout, rows, &p.seg)) != MOE_OK) return st;
   if (!grad_x && !grad_weight && !grad_bias) return MOE_ERR_INVALID_ARG;
   if (!maybe_rows_ok(grad_x) || !maybe_rows_ok(grad_weight) || !aligned16(grad_bias))

@@ -329,47 +329,111 @@ struct Fp8Product {
   }
 };
 
-// gz = grad_y * act'(pre) to bf16, and its column sums in fp32: a thread owns
-// one column and the block walks the expert's rows.
+// ---------------------------------------------------------------------------
+// gz = grad_y * act'(pre) to bf16, and its column sums in fp32 (summed before
+// that rounding).  A stream: a lane owns 8 columns (of the gate and of the up
+// half), a block 4 x 512 columns of every split's rows, four rows on their way
+// at once; the splits' sums are added by a second launch.
+// ---------------------------------------------------------------------------
+constexpr int kActRows = 4;
+
+__device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == kActSilu) {
+    const float s = sigmoid_f32(z);
+    return s * (1.0f + z * (1.0f - s));
+  }
+  if (ACT == kActGelu)
+    return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+           z * expf(-0.5f * z * z) * 0.39894228040143268f;
+  return 1.0f;
+}
+
+// parts: [gridDim.z][E][P] column sums, or NULL when they are not wanted.
 template <int ACT>
 __global__ void __launch_bounds__(kThreads)
-act_grad_kernel(MatmulGradParams p, uint16_t* gz) {
-  const int e = blockIdx.y;
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= p.F) return;
+act_grad_kernel(MatmulGradParams p, uint16_t* gz, float* parts) {
+  constexpr bool kGated = ACT == kActSwiglu;
+  __shared__ __align__(16) float s_sum[kActRows - 1][kGated ? 2 : 1][kWave * 8];
+  const int e = blockIdx.y, lane = lane_id(), wave = threadIdx.x / kWave;
+  const int c = (blockIdx.x * kWave + lane) * 8;
+  const bool in = c < p.F;
   int begin, end;
   segment_of(p.seg, e, begin, end);
-  float sum0 = 0.0f, sum1 = 0.0f;
-  for (int m = begin; m < end; ++m) {
-    const float gy = bf16_f32(p.grad_y[(size_t)m * p.F + c]);
-    const size_t at = (size_t)m * p.P + c;
-    if constexpr (ACT == kActSwiglu) {
-      const float g = bf16_f32(p.pre[at]), u = bf16_f32(p.pre[at + p.F]);
-      const float s = sigmoid_f32(g);
-      const float dg = gy * u * s * (1.0f + g * (1.0f - s)), du = gy * g * s;
-      gz[at] = (uint16_t)pack_bf16x2(dg, 0.0f);
-      gz[at + p.F] = (uint16_t)pack_bf16x2(du, 0.0f);
-      sum0 += dg;
-      sum1 += du;
-    } else {
-      float d = gy;
-      if constexpr (ACT == kActSilu) {
-        const float z = bf16_f32(p.pre[at]);
-        const float s = sigmoid_f32(z);
-        d = gy * s * (1.0f + z * (1.0f - s));
-      } else if constexpr (ACT == kActGelu) {
-        const float z = bf16_f32(p.pre[at]);
-        d = gy * (0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-                  z * expf(-0.5f * z * z) * 0.39894228040143268f);
+  const int per = (max(end - begin, 0) + gridDim.z - 1) / gridDim.z;
+  const int first = begin + blockIdx.z * per, last = min(first + per, end);
+  float sum[8] = {}, sum_up[8] = {};
+  if (in) {
+    for (int m = first + wave; m < last; m += kActRows) {
+      float gy[8], z[8], up[8], d[8], du[8];
+      load8(gy, p.grad_y + (size_t)m * p.F + c);
+      const size_t at = (size_t)m * p.P + c;
+      if (ACT != kActNone) load8(z, p.pre + at);
+      if (kGated) load8(up, p.pre + at + p.F);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (kGated) {
+          const float s = sigmoid_f32(z[i]);
+          d[i] = gy[i] * up[i] * s * (1.0f + z[i] * (1.0f - s));
+          du[i] = gy[i] * z[i] * s;
+          sum_up[i] += du[i];
+        } else {
+          d[i] = ACT == kActNone ? gy[i] : gy[i] * act_slope<ACT>(z[i]);
+        }
+        sum[i] += d[i];
       }
-      if (gz) gz[at] = (uint16_t)pack_bf16x2(d, 0.0f);
-      sum0 += d;
+      if (ACT != kActNone) store8(gz + at, d);
+      if (kGated) store8(gz + at + p.F, du);
     }
   }
-  if (p.grad_bias) {
-    p.grad_bias[(size_t)e * p.P + c] = sum0;
-    if constexpr (ACT == kActSwiglu) p.grad_bias[(size_t)e * p.P + p.F + c] = sum1;
+  if (!parts) return;
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s_sum[wave - 1][0][lane * 8 + i] = sum[i];
+      if (kGated) s_sum[wave - 1][kGated ? 1 : 0][lane * 8 + i] = sum_up[i];
+    }
   }
+  __syncthreads();
+  if (wave > 0 || !in) return;
+  float* out = parts + ((size_t)blockIdx.z * p.seg.E + e) * p.P + c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    for (int w = 0; w < kActRows - 1; ++w) {
+      sum[i] += s_sum[w][0][lane * 8 + i];
+      if (kGated) sum_up[i] += s_sum[w][kGated ? 1 : 0][lane * 8 + i];
+    }
+    out[i] = sum[i];
+    if (kGated) out[p.F + i] = sum_up[i];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+bias_grad_kernel(const float* parts, float* grad_bias, size_t n, int splits) {
+  const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) sum += parts[(size_t)s * n + i];
+  grad_bias[i] = sum;
+}
+
+// Splits of an expert's rows: enough blocks to fill the chip, no fewer than 16
+// rows to a split on average.
+int act_splits(int pairs, int E, int F) {
+  const int64_t blocks = (int64_t)E * ((F + 511) / 512);
+  const int64_t want = (2048 + blocks - 1) / blocks, most = pairs / E / 16 + 1;
+  return (int)(want < most ? want : most);
 }
 
 // y (and pre): u runs over weight rows; a gated layer's wave takes half of its
@@ -570,6 +634,13 @@ using Small = Config<2, 2, 8, 4>;
 
 // Large tiles where an expert has more rows than one small tile on average
 // and the large tiles alone fill the 256 compute units.
+#ifndef GXL
+#define GXL Large
+#endif
+#ifndef GWL
+#define GWL Large
+#endif
+using Mid = Config<2, 2, 4, 4>;
 // fp8: 128 weight rows by 256 token rows, so that an expert's weights are read
 // once however its 128 or so rows fall.
 using Codes = Config<2, 4, 4, 4>;
@@ -644,28 +715,48 @@ hipError_t launch_expert_matmul(const MatmulParams& p, bool fp8, hipStream_t st)
   }
 }
 
+size_t gz_bytes(int rows, int P, int act) {
+  return act == kActNone ? 0 : ((size_t)rows * P * 2 + 15) / 16 * 16;
+}
+
 size_t expert_matmul_grad_workspace(int rows, int pairs, int E, int P, int act) {
-  return act == kActNone || pairs == 0 ? 0 : ((size_t)rows * P * 2 + 15) / 16 * 16;
+  if (pairs == 0) return 0;
+  const int splits = act_splits(pairs, E, act == kActSwiglu ? P / 2 : P);
+  return gz_bytes(rows, P, act) + (splits > 1 ? (size_t)splits * E * P * 4 : 0);
 }
 
 hipError_t launch_expert_matmul_grad(const MatmulGradParams& p, hipStream_t st) {
   uint16_t* gz = p.act == kActNone ? nullptr : static_cast<uint16_t*>(p.workspace);
   if (p.grad_bias || p.act != kActNone) {
-    const dim3 grid((p.F + kThreads - 1) / kThreads, p.seg.E);
+    const int splits = p.seg.pairs == 0 ? 1 : act_splits(p.seg.pairs, p.seg.E, p.F);
+    float* parts = !p.grad_bias ? nullptr
+                   : splits == 1
+                       ? p.grad_bias
+                       : reinterpret_cast<float*>(static_cast<char*>(p.workspace) +
+                                                  gz_bytes(p.seg.rows, p.P, p.act));
+    const dim3 grid((p.F + 511) / 512, p.seg.E, splits);
+#define MOE_ACT_GRAD(ACT)                                                                     \
+  hipLaunchKernelGGL((act_grad_kernel<ACT>), grid, dim3(kThreads), 0, st, p, gz, parts)
     switch (p.act) {
-      case kActSilu: hipLaunchKernelGGL((act_grad_kernel<kActSilu>), grid, dim3(kThreads), 0, st, p, gz); break;
-      case kActGelu: hipLaunchKernelGGL((act_grad_kernel<kActGelu>), grid, dim3(kThreads), 0, st, p, gz); break;
-      case kActSwiglu: hipLaunchKernelGGL((act_grad_kernel<kActSwiglu>), grid, dim3(kThreads), 0, st, p, gz); break;
-      default: hipLaunchKernelGGL((act_grad_kernel<kActNone>), grid, dim3(kThreads), 0, st, p, gz); break;
+      case kActSilu: MOE_ACT_GRAD(kActSilu); break;
+      case kActGelu: MOE_ACT_GRAD(kActGelu); break;
+      case kActSwiglu: MOE_ACT_GRAD(kActSwiglu); break;
+      default: MOE_ACT_GRAD(kActNone); break;
+    }
+#undef MOE_ACT_GRAD
+    if (p.grad_bias && splits > 1) {
+      const size_t n = (size_t)p.seg.E * p.P;
+      hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)),
+                         dim3(kThreads), 0, st, parts, p.grad_bias, n, splits);
     }
   }
   const uint16_t* g = gz ? gz : p.grad_y;
   const bool large = large_tiles(p.seg, p.K);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.grad_x)
-    e = large ? launch_grad_x<Large>(p, g, st) : launch_grad_x<Small>(p, g, st);
+    e = large ? launch_grad_x<GXL>(p, g, st) : launch_grad_x<Small>(p, g, st);
   if (e == hipSuccess && p.grad_weight)
-    e = (int64_t)p.K * p.P >= 256 * 256 ? launch_grad_w<Large>(p, g, st)
+    e = (int64_t)p.K * p.P >= 256 * 256 ? launch_grad_w<GWL>(p, g, st)
                                         : launch_grad_w<Small>(p, g, st);
   return e;
 }

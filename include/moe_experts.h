@@ -101,7 +101,8 @@ size_t moe_expert_matmul_backward_workspace_size(const moe_shape *shape,
  *   workspace     moe_expert_matmul_backward_workspace_size bytes, 16-byte
  *                 aligned; contents need no initialisation.  It holds gz
  *                 rounded to bf16, which the two products read (grad_bias is
- *                 summed before that rounding).
+ *                 summed before that rounding), and parts of those sums.  NULL
+ *                 is allowed for MOE_ACT_NONE without grad_bias.
  */
 moe_status moe_expert_matmul_backward(const moe_shape *shape, const moe_linear *linear,
                                       const void *grad_y, const void *x,
