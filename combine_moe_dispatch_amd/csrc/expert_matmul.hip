@@ -55,31 +55,36 @@ struct TileProduct {
   typename A::template Reader<C::kTu> ra;
   typename B::template Reader<C::kTv> rb;
 
-  // Fragment i (of kTv + kTu) of part k of the step at lds.
-  template <bool TAIL>
+  // A tile whose second half has no rows (only where B's rows run along r) takes
+  // half of the products and of B's loads: PART is how much of the fragments
+  // along v a wave has to do, kTv or kTv / 2.
+  template <int PART>
+  static constexpr int kPartLoads = A::kLoads + B::kLoads * PART / C::kTv;
+
+  // Fragment i (of PART + kTu) of part k of the step at lds.
+  template <int PART, bool TAIL>
   __device__ __forceinline__ void read(Fragments& f, int i, uint32_t lds, int k, int left) const {
-    if (i < C::kTv)
+    if (i < PART)
       f.b[i] = rb.template frag<TAIL>(lds + A::kBytes, i * (BT ? 1 : C::kWv), k, left);
     else
-      f.a[i - C::kTv] = ra.template frag<TAIL>(lds, i - C::kTv, k, left);
+      f.a[i - PART] = ra.template frag<TAIL>(lds, i - PART, k, left);
   }
-  template <bool TAIL>
+  template <int PART, bool TAIL>
   __device__ __forceinline__ void read_all(Fragments& f, uint32_t lds, int k, int left) const {
 #pragma unroll
-    for (int i = 0; i < C::kTv + C::kTu; ++i) read<TAIL>(f, i, lds, k, left);
+    for (int i = 0; i < PART + C::kTu; ++i) read<PART, TAIL>(f, i, lds, k, left);
   }
 
   // acc += f, row of fragments by row, with before(u) in front of row u: what
   // it issues runs beside the products.
-  template <class Before>
+  template <int PART, class Before>
   __device__ __forceinline__ void multiply(const Fragments& f, Before before) {
 #pragma unroll
     for (int u = 0; u < C::kTu; ++u) {
       before(u);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int v = 0; v < C::kTv; ++v)
-        mfma_in_place(acc[u][v], f.a[u], f.b[v]);
+      for (int v = 0; v < PART; ++v) mfma_in_place(acc[u][v], f.a[u], f.b[v]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -91,42 +96,67 @@ struct TileProduct {
       for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
   }
 
-  // red > 0 positions along r.  ap[i] is where load i of this wave starts in A
-  // (weight rows of a gated layer lie in two places), bp in B; lda, ldb are
-  // the operands' row pitches in bytes.
-  __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
-                                      const char* bp, uint32_t lda, uint32_t ldb, int red) {
-    static_assert(kParts == 2, "the parts are written out");
+  // A tile's operands: ap[i] is where load i of this wave starts in A (weight
+  // rows of a gated layer lie in two places), bp in B; lda, ldb are the
+  // operands' row pitches in bytes, red > 0 the positions along r.
+  const char* ap[A::kLoads];
+  const char* bp;
+  uint32_t lda, ldb;
+  int red, wave;
+  uint32_t lds;
+
+  __device__ __forceinline__ void setup(char* smem, int wave_) {
+    wave = wave_;
+    lds = lds_address(smem);
     ra.init(wave % C::kWu * C::kTu * 16);
     rb.init(wave / C::kWu * 16, C::kWv);
+  }
+  __device__ __forceinline__ int steps() const { return (red + kStep - 1) / kStep; }
+  // The next step's load i, and all of them.
+  template <bool TAIL>
+  __device__ __forceinline__ void load(int i, uint32_t to) {
+    const int rest = red % kStep;
+    if (i < A::kLoads)
+      a.template load<TAIL>(i, to, wave, ap[i], lda, rest);
+    else if (i < kLoads)
+      b.template load<TAIL>(i - A::kLoads, to + A::kBytes, wave, bp, ldb, rest);
+  }
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int i = 0; i < A::kLoads; ++i) ap[i] += AT ? (size_t)kStep * lda : (size_t)kStep * 2;
+    bp += BT ? (size_t)kStep * ldb : (size_t)kStep * 2;
+  }
+  template <int PART>
+  __device__ __forceinline__ void start(uint32_t to, bool full) {
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < kPartLoads<PART>; ++i) load<false>(i, to);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPartLoads<PART>; ++i) load<true>(i, to);
+    }
+    advance();
+  }
+  // Start the first two steps of a tile.  No wave may still read LDS.
+  template <int PART>
+  __device__ __forceinline__ void begin() {
+    const int whole = red / kStep;
+    start<PART>(lds, whole > 0);
+    if (steps() > 1) start<PART>(lds + kStage, whole > 1);
+  }
+
+  // The tile that begin() has started.  Afterwards LDS is free again.  behind:
+  // stores that this wave has started since (0, or kStores at least).
+  template <int PART>
+  __device__ __forceinline__ void run(int behind) {
+    constexpr int kLoads = kPartLoads<PART>;
+    constexpr int kBehind = C::kTv * C::kTu / 2;
+    static_assert(kLoads + kBehind < 64, "counted by the hardware");
+    static_assert(kParts == 2, "the parts are written out");
     clear();
-    const size_t sta = AT ? (size_t)kStep * lda : (size_t)kStep * 2;
-    const size_t stb = BT ? (size_t)kStep * ldb : (size_t)kStep * 2;
-    uint32_t here = lds_address(smem), next = here + kStage;
-    const int steps = (red + kStep - 1) / kStep;
-    const int rest = red - (steps - 1) * kStep;       // positions of the last step
-    const int whole = rest == kStep ? steps : steps - 1;
-    auto advance = [&] {
-#pragma unroll
-      for (int i = 0; i < A::kLoads; ++i) ap[i] += sta;
-      bp += stb;
-    };
-    auto load = [&](int i, uint32_t to, auto tail) {  // load i of the next step
-      if (i < A::kLoads)
-        a.template load<decltype(tail)::value>(i, to, wave, ap[i], lda, rest);
-      else if (i < kLoads)
-        b.template load<decltype(tail)::value>(i - A::kLoads, to + A::kBytes, wave, bp, ldb, rest);
-    };
-    auto start = [&](uint32_t to, bool full) {
-      if (full) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) load(i, to, std::false_type{});
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) load(i, to, std::true_type{});
-      }
-      advance();
-    };
+    uint32_t here = lds, next = lds + kStage;
+    const int steps = this->steps(), whole = red / kStep;
+    const int rest = red - (steps - 1) * kStep;  // positions of the last step
     // Every wave's reads of `here` are in registers and its loads of `next` in
     // LDS: `here` may be filled again and `next` be read.
     auto meet = [&] {
@@ -140,63 +170,78 @@ struct TileProduct {
       here = next;
       next = h;
     };
-    constexpr int kReads = (2 * (C::kTu + C::kTv) + C::kTu - 1) / C::kTu;  // in the first rows
+    constexpr int kReads = (2 * (C::kTu + PART) + C::kTu - 1) / C::kTu;  // in the first rows
     constexpr int kStarts = (kLoads + C::kTu - 1) / C::kTu;
     auto reading = [&](Fragments& f, uint32_t lds, int k, int u) {
 #pragma unroll
       for (int i = u * kReads; i < (u + 1) * kReads; ++i)
-        if (i < C::kTu + C::kTv) read<false>(f, i, lds, k, rest);
+        if (i < C::kTu + PART) read<PART, false>(f, i, lds, k, rest);
     };
     const auto nothing = [](int) {};
     Fragments f0, f1;
-    start(here, whole > 0);
-    if (steps > 1) {
-      start(next, whole > 1);
+    if (steps > 1 && behind > 0)
+      wait_vm<kLoads + kBehind>();
+    else if (steps > 1)
       wait_vm<kLoads>();
-    } else {
+    else
       wait_vm<0>();
-    }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if (steps > 1)
-      read_all<false>(f0, here, 0, rest);
+      read_all<PART, false>(f0, here, 0, rest);
     else
-      read_all<true>(f0, here, 0, rest);
+      read_all<PART, true>(f0, here, 0, rest);
     // Half a step is multiplied while the next half is read, the second half
     // behind the barrier, so that the matrix units have work on both sides.
     for (int t = 0; t + 2 < whole; ++t) {
-      multiply(f0, [&](int u) { reading(f1, here, 1, u); });
+      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
       meet();
-      multiply(f1, [&](int u) {
+      multiply<PART>(f1, [&](int u) {
         reading(f0, next, 0, u);
 #pragma unroll
-        for (int i = u * kStarts; i < (u + 1) * kStarts; ++i) load(i, here, std::false_type{});
+        for (int i = u * kStarts; i < (u + 1) * kStarts; ++i)
+          if (i < kLoads) load<false>(i, here);
       });
       advance();
       turn();
     }
     if (whole < steps && steps > 2) {  // the step whose loads are the short ones
-      multiply(f0, [&](int u) { reading(f1, here, 1, u); });
+      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
       meet();
-      start(here, false);
-      multiply(f1, [&](int u) { reading(f0, next, 0, u); });
+      start<PART>(here, false);
+      multiply<PART>(f1, [&](int u) { reading(f0, next, 0, u); });
       turn();
     }
     if (steps > 1) {
-      multiply(f0, [&](int u) { reading(f1, here, 1, u); });
+      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
       meet();
-      multiply(f1, nothing);
-      read_all<true>(f0, next, 0, rest);
+      multiply<PART>(f1, nothing);
+      read_all<PART, true>(f0, next, 0, rest);
       turn();
     }
-    read_all<true>(f1, here, 1, rest);
-    multiply(f0, nothing);
-    multiply(f1, nothing);
+    read_all<PART, true>(f1, here, 1, rest);
+    multiply<PART>(f0, nothing);
+    wait_lds();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    multiply<PART>(f1, nothing);
     mfma_results();
 #pragma unroll
     for (int u = 0; u < C::kTu; ++u)
 #pragma unroll
       for (int v = 0; v < C::kTv; ++v) mfma_result(acc[u][v]);
+  }
+
+  // A tile of `rows` along v, from its first load on.
+  __device__ __forceinline__ void begin_and_run(int rows) {
+    static_assert(!BT, "the front of a transposed operand's tile is not its first columns");
+    if (rows > C::kBv / 2) {
+      begin<C::kTv>();
+      run<C::kTv>(0);
+    } else {
+      begin<C::kTv / 2>();
+      run<C::kTv / 2>(0);
+    }
   }
 
   // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours
@@ -454,7 +499,7 @@ __device__ __forceinline__ void weight_loads(A& a, const char* (&ap)[A::kLoads],
   using Cols = Columns<C, ACT>;
 #pragma unroll
   for (int i = 0; i < A::kLoads; ++i) {
-    const int q = wave * A::kLoads + i;
+    const int q = A::load_of(i, wave);
     int row, c;
     A::chunk_of(q, row, c);
     const int first = q * A::kRowsPerLoad;  // the load's rows are of one kind
@@ -506,20 +551,21 @@ __device__ __forceinline__ void finish(const Product& prod, const MatmulParams& 
 template <class C, int ACT>
 __global__ void __launch_bounds__(C::kThreads)
 matmul_kernel(MatmulParams p, int ntiles) {
-  using Product = TileProduct<C, false, false>;
   extern __shared__ __align__(1024) char smem[];
   Tile t;
   if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n0 = t.n * Columns<C, ACT>::kTile;
-  const uint32_t ld = (uint32_t)p.K * 2;
-  Product prod;
-  const char* ap[Product::A::kLoads];
-  weight_loads<C, ACT>(prod.a, ap,
-                       static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld, wave,
-                       p.F, p.F - n0, ld);
-  prod.b.init(wave, ld, min(C::kBv, t.end - t.m0));
-  prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, ld, ld, p.K);
+  TileProduct<C, false, false> prod;
+  prod.setup(smem, wave);
+  prod.lda = prod.ldb = (uint32_t)p.K * 2;
+  prod.red = p.K;
+  weight_loads<C, ACT>(prod.a, prod.ap,
+                       static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * prod.lda,
+                       wave, p.F, p.F - n0, prod.lda);
+  prod.b.init(wave, prod.ldb, min(C::kBv, t.end - t.m0));
+  prod.bp = static_cast<const char*>(p.x) + (size_t)t.m0 * prod.ldb;
+  prod.begin_and_run(t.end - t.m0);
   finish<C, ACT>(prod, p, t, wave);
 }
 
@@ -555,21 +601,24 @@ matmul_fp8_kernel(MatmulParams p, int ntiles) {
 }
 
 // The accumulators as bf16 rows: row v of the tile to out + v * ld, for v
-// below rows, columns below cols.
-template <class C, class Product>
+// below rows, columns below cols.  A whole tile takes kStores stores a lane.
+template <class C>
+constexpr int kStores = C::kTv * C::kTu / 2;
+
+template <class C, bool WHOLE, class Product>
 __device__ __forceinline__ void store_tile(const Product& prod, int wave, uint16_t* out, size_t ld,
                                            int rows, int cols) {
   const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
 #pragma unroll
   for (int v = 0; v < C::kTv; ++v) {
     const int m = (v * C::kWv + wv) * 16 + (lane & 15);
-    if (m >= rows) continue;
+    if (!WHOLE && m >= rows) continue;
 #pragma unroll
     for (int a = 0; a < C::kTu / 2; ++a) {
       const int c = (wu * C::kTu + 2 * a) * 16 + (lane >> 4) * 8;
       float o[8];
       prod.eight(o, a, v);
-      if (c < cols) store8(out + (size_t)m * ld + c, o);
+      if (WHOLE || c < cols) store8(out + (size_t)m * ld + c, o);
     }
   }
 }
@@ -584,47 +633,89 @@ grad_x_kernel(MatmulGradParams p, const uint16_t* gz, int ntiles) {
   if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n0 = t.n * C::kBu;
-  const uint32_t lda = (uint32_t)p.K * 2, ldb = (uint32_t)p.P * 2;
   Product prod;
-  prod.a.init(wave, lda, min(C::kBu, p.K - n0));
-  prod.b.init(wave, ldb, min(C::kBv, t.end - t.m0));
-  const char* ap[Product::A::kLoads];
+  prod.setup(smem, wave);
+  prod.lda = (uint32_t)p.K * 2;
+  prod.ldb = (uint32_t)p.P * 2;
+  prod.red = p.P;
+  prod.a.init(wave, prod.lda, min(C::kBu, p.K - n0));
+  prod.b.init(wave, prod.ldb, min(C::kBv, t.end - t.m0));
 #pragma unroll
   for (int i = 0; i < Product::A::kLoads; ++i)
-    ap[i] = reinterpret_cast<const char*>(p.weight + (size_t)t.e * p.P * p.K + n0);
-  prod.run(smem, wave, ap, reinterpret_cast<const char*>(gz) + (size_t)t.m0 * ldb, lda, ldb, p.P);
-  store_tile<C>(prod, wave, p.grad_x + (size_t)t.m0 * p.K + n0, p.K, t.end - t.m0, p.K - n0);
+    prod.ap[i] = reinterpret_cast<const char*>(p.weight + (size_t)t.e * p.P * p.K + n0);
+  prod.bp = reinterpret_cast<const char*>(gz + (size_t)t.m0 * p.P);
+  prod.begin_and_run(t.end - t.m0);
+  store_tile<C, false>(prod, wave, p.grad_x + (size_t)t.m0 * p.K + n0, p.K, t.end - t.m0,
+                       p.K - n0);
 }
 
-// grad_w: D[input feature][weight row], summed over the expert's rows.
+// grad_w: D[input feature][weight row], summed over the expert's rows.  Every
+// expert has nt x pt tiles; one without rows has zeros.  With few rows an
+// expert a tile is a handful of steps and a large result, so the blocks stay:
+// each takes one tile after another and starts the loads of the next before
+// it stores the last, without waiting for those stores.
 template <class C>
 __global__ void __launch_bounds__(C::kThreads)
 grad_w_kernel(MatmulGradParams p, const uint16_t* gz, unsigned nt, unsigned pt) {
   using Product = TileProduct<C, true, true>;
   extern __shared__ __align__(1024) char smem[];
-  const unsigned b = xcd_local_block(blockIdx.x, gridDim.x);
-  const int e = (int)(b / (nt * pt));
-  const unsigned in = b % (nt * pt);
-  const int n0 = (int)(in / pt) * C::kBu, p0 = (int)(in % pt) * C::kBv;
-  int begin, end;
-  segment_of(p.seg, e, begin, end);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const uint32_t lda = (uint32_t)p.K * 2, ldb = (uint32_t)p.P * 2;
+  int* seg_begin = reinterpret_cast<int*>(smem + Product::kLds);
+  int* seg_rows = seg_begin + kMaxExperts;
+  fill_table(seg_begin, seg_rows, p.seg);
+  __syncthreads();
+  const unsigned total = nt * pt * (unsigned)p.seg.E;
   Product prod;
-  if (end > begin) {
-    prod.a.init(wave, lda, min(C::kBu, p.K - n0));
-    prod.b.init(wave, ldb, min(C::kBv, p.P - p0));
-    const char* ap[Product::A::kLoads];
+  prod.setup(smem, wave);
+  prod.lda = (uint32_t)p.K * 2;
+  prod.ldb = (uint32_t)p.P * 2;
+  struct Place {
+    int e, n0, p0, rows;
+  };
+  auto place = [&](unsigned b) {
+    const unsigned at = xcd_local_block(b, total), in = at % (nt * pt);
+    Place w;
+    w.e = (int)(at / (nt * pt));
+    // neighbouring blocks write neighbouring columns (897 against 1000 us the
+    // other way round at 32 experts, 4096 x 7168)
+    w.n0 = (int)(in % nt) * C::kBu;
+    w.p0 = (int)(in / nt) * C::kBv;
+    w.rows = __builtin_amdgcn_readfirstlane(seg_rows[w.e]);
+    return w;
+  };
+  auto begin = [&](const Place& w) {
+    if (w.rows <= 0) return;
+    const int first = __builtin_amdgcn_readfirstlane(seg_begin[w.e]);
+    prod.red = w.rows;
+    prod.a.init(wave, prod.lda, min(C::kBu, p.K - w.n0));
+    prod.b.init(wave, prod.ldb, min(C::kBv, p.P - w.p0));
 #pragma unroll
     for (int i = 0; i < Product::A::kLoads; ++i)
-      ap[i] = reinterpret_cast<const char*>(p.x + (size_t)begin * p.K + n0);
-    prod.run(smem, wave, ap, reinterpret_cast<const char*>(gz + (size_t)begin * p.P + p0), lda,
-             ldb, end - begin);
-  } else {
-    prod.clear();
+      prod.ap[i] = reinterpret_cast<const char*>(p.x + (size_t)first * p.K + w.n0);
+    prod.bp = reinterpret_cast<const char*>(gz + (size_t)first * p.P + w.p0);
+    prod.template begin<C::kTv>();
+  };
+  Place w = place(blockIdx.x);  // the grid has no more blocks than tiles
+  begin(w);
+  bool stores = false;  // kStores of them started behind this tile's loads
+  for (unsigned b = blockIdx.x;;) {
+    if (w.rows > 0)
+      prod.template run<C::kTv>(stores ? kStores<C> : 0);
+    else
+      prod.clear();
+    b += gridDim.x;
+    const bool more = b < total;
+    const Place n = place(more ? b : 0);
+    if (more) begin(n);
+    uint16_t* out = p.grad_weight + ((size_t)w.e * p.P + w.p0) * p.K + w.n0;
+    stores = p.P - w.p0 >= C::kBv && p.K - w.n0 >= C::kBu;
+    if (stores)
+      store_tile<C, true>(prod, wave, out, p.K, 0, 0);
+    else
+      store_tile<C, false>(prod, wave, out, p.K, p.P - w.p0, p.K - w.n0);
+    if (!more) break;
+    w = n;
   }
-  store_tile<C>(prod, wave, p.grad_weight + ((size_t)e * p.P + p0) * p.K + n0, p.K, p.P - p0,
-                p.K - n0);
 }
 
 // 256 x 256 tiles for experts of many rows, 256 x 128 for those of few: a part
@@ -656,26 +747,41 @@ hipError_t allow_lds(K kernel, int bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <class C, int ACT, class Product, class Kernel>
-hipError_t launch_tiles(Kernel kernel, const MatmulParams& p, hipStream_t st) {
+constexpr int kUnits = 256;  // compute units
+
+template <class C, int ACT>
+hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
   constexpr int kCols = Columns<C, ACT>::kTile;
+  constexpr int kLds = TileProduct<C, false, false>::kLds;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds(kernel, Product::kLds);
+  const hipError_t e = allow_lds(matmul_kernel<C, ACT>, kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(C::kThreads), Product::kLds, st, p, ntiles);
+  hipLaunchKernelGGL((matmul_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p,
+                     ntiles);
+  return hipGetLastError();
+}
+
+template <class C, int ACT>
+hipError_t launch_codes(const MatmulParams& p, hipStream_t st) {
+  constexpr int kCols = Columns<C, ACT>::kTile;
+  constexpr int kLds = Fp8Product<C>::kLds;
+  const int ntiles = (p.F + kCols - 1) / kCols;
+  const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  const hipError_t e = allow_lds(matmul_fp8_kernel<C, ACT>, kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((matmul_fp8_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds,
+                     st, p, ntiles);
   return hipGetLastError();
 }
 
 template <int ACT>
 hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
-  if (fp8) return launch_tiles<Codes, ACT, Fp8Product<Codes>>(matmul_fp8_kernel<Codes, ACT>, p, st);
-  if (large_tiles(p.seg, p.P))
-    return launch_tiles<Large, ACT, TileProduct<Large, false, false>>(matmul_kernel<Large, ACT>, p,
-                                                                      st);
-  return launch_tiles<Small, ACT, TileProduct<Small, false, false>>(matmul_kernel<Small, ACT>, p,
-                                                                    st);
+  if (fp8) return launch_codes<Codes, ACT>(p, st);
+  if (large_tiles(p.seg, p.P)) return launch_tiles<Large, ACT>(p, st);
+  return launch_tiles<Small, ACT>(p, st);
 }
 
 template <class C>
@@ -693,14 +799,14 @@ hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStrea
 
 template <class C>
 hipError_t launch_grad_w(const MatmulGradParams& p, const uint16_t* gz, hipStream_t st) {
-  constexpr int kLds = TileProduct<C, true, true>::kLds;
+  constexpr int kLds = TileProduct<C, true, true>::kLds + kTableBytes;
   const unsigned nt = (p.K + C::kBu - 1) / C::kBu, pt = (p.P + C::kBv - 1) / C::kBv;
-  const int64_t grid = (int64_t)nt * pt * p.seg.E;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  const int64_t tiles = (int64_t)nt * pt * p.seg.E;
+  if (tiles > INT32_MAX) return hipErrorInvalidValue;
   const hipError_t e = allow_lds(grad_w_kernel<C>, kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((grad_w_kernel<C>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p, gz,
-                     nt, pt);
+  hipLaunchKernelGGL((grad_w_kernel<C>), dim3((unsigned)(tiles < kUnits ? tiles : kUnits)),
+                     dim3(C::kThreads), kLds, st, p, gz, nt, pt);
   return hipGetLastError();
 }
 

@@ -66,6 +66,19 @@ __device__ __forceinline__ bool find_tile(const Segments& s, int ntiles, unsigne
   return false;
 }
 
+// Every expert's rows in LDS, for blocks that take one tile after another: a
+// look at the counts in memory would wait for the block's loads and stores
+// under way.  A barrier has to follow.
+constexpr int kTableBytes = 2 * kMaxExperts * 4;
+__device__ __forceinline__ void fill_table(int* begin, int* rows, const Segments& s) {
+  for (int e = threadIdx.x; e < s.E; e += blockDim.x) {
+    int first, end;
+    segment_of(s, e, first, end);
+    begin[e] = first;
+    rows[e] = end - first;
+  }
+}
+
 // Most tiles a grouped product can have: every expert may end in a part tile.
 inline int64_t tile_bound(const Segments& s, int bv, int ntiles) {
   const int64_t busy = s.E < s.pairs ? s.E : s.pairs;
@@ -141,6 +154,8 @@ struct OperandTile {
     if (TRANSPOSED) return ((row & 3) | ((row >> 3) & 1) << 2) << 1;
     return PAIRED ? ((row >> 1) & 1) | ((row >> 3) & 3) << 1 : (row >> 1) & 7;
   }
+  // Load i of a wave among the tile's: the waves' first loads fill its front.
+  static __device__ __forceinline__ int load_of(int i, int wave) { return i * WAVES + wave; }
   // The chunk that this lane brings in with load q of the tile, and its row.
   static __device__ __forceinline__ void chunk_of(int q, int& row, int& c) {
     const int lane = lane_id();
@@ -155,7 +170,7 @@ struct OperandTile {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       int row, c;
-      chunk_of(wave * kLoads + i, row, c);
+      chunk_of(load_of(i, wave), row, c);
       if constexpr (TRANSPOSED) {
         off[i] = (uint32_t)row * ld + (uint32_t)min(c * 8, valid - 8) * 2;
         where[i] = (uint16_t)row;
@@ -173,7 +188,7 @@ struct OperandTile {
     uint32_t o = off[i];
     if (TAIL && (int)where[i] >= left)
       o -= TRANSPOSED ? (uint32_t)where[i] * ld : (uint32_t)where[i] * 2;
-    load_to_lds(lds + (uint32_t)(wave * kLoads + i) * 1024, base, o);
+    load_to_lds(lds + (uint32_t)load_of(i, wave) * 1024, base, o);
   }
 
   // Reading fragments: N of 16 rows each (columns, when transposed) from i0
