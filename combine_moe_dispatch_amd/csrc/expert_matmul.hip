@@ -253,6 +253,129 @@ struct TileProduct {
 };
 
 // ---------------------------------------------------------------------------
+// The product for few rows an expert, where the weights' way from memory is
+// what counts.  Each of a block's SPLIT waves takes a share of the steps for
+// the whole tile, through a ring of its own in LDS: no wave waits for another
+// until the shares are added up, and a tile that has a compute unit to itself
+// still has SPLIT rings of loads on their way.
+// ---------------------------------------------------------------------------
+template <int TU, int TV, int SPLIT, int STAGES>
+struct StreamProduct {
+  using C = Config<1, 1, TU, TV>;  // of one wave
+  using A = OperandTile<C::kBu, 1, false, true>;
+  using B = OperandTile<C::kBv, 1, false, false>;
+  static constexpr int kThreads = SPLIT * kWave;
+  static constexpr int kStage = A::kBytes + B::kBytes;
+  static constexpr int kRing = STAGES * kStage;
+  static constexpr int kLds = SPLIT * kRing;
+  static constexpr int kLoads = A::kLoads + B::kLoads;
+  static_assert((STAGES - 2) * kLoads < 64, "counted by the hardware");
+  A a;
+  B b;
+  f32x4_t acc[TU][TV];
+  typename A::template Reader<TU> ra;
+  typename B::template Reader<TV> rb;
+
+  template <bool TAIL>
+  __device__ __forceinline__ void multiply(uint32_t here, int nv, int left) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      bf16x8_t fa[TU];
+#pragma unroll
+      for (int u = 0; u < TU; ++u) fa[u] = ra.template frag<TAIL>(here, u, k, left);
+#pragma unroll
+      for (int v = 0; v < TV; ++v) {
+        if (v >= nv) break;
+        const bf16x8_t fb = rb.template frag<TAIL>(here + A::kBytes, v, k, left);
+#pragma unroll
+        for (int u = 0; u < TU; ++u)
+          acc[u][v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u], fb, acc[u][v], 0, 0, 0);
+      }
+    }
+  }
+
+  // red > 0 positions along r, `rows` rows along v; ap, bp as in TileProduct.
+  // Wave 0 is left with the result.
+  __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
+                                      const char* bp, int red, int rows) {
+    ra.init(0);
+    rb.init(0);
+#pragma unroll
+    for (int u = 0; u < TU; ++u)
+#pragma unroll
+      for (int v = 0; v < TV; ++v) acc[u][v] = f32x4_t{};
+    const int nv = min((rows + 15) / 16, TV);
+    const int steps = (red + kStep - 1) / kStep;
+    const int rest = red - (steps - 1) * kStep;  // positions of the last step
+    const int share = (steps + SPLIT - 1) / SPLIT;
+    const int first = min(wave * share, steps), end = min(first + share, steps);
+#pragma unroll
+    for (int i = 0; i < A::kLoads; ++i) ap[i] += (size_t)first * (kStep * 2);
+    bp += (size_t)first * (kStep * 2);
+    const uint32_t lds = lds_address(smem) + wave * kRing, lds_end = lds + kRing;
+    uint32_t fill = lds, here = lds;
+    auto after = [&](uint32_t slot) { return slot + kStage == lds_end ? lds : slot + kStage; };
+    auto load = [&](auto tail) {
+      constexpr bool kTail = decltype(tail)::value;
+#pragma unroll
+      for (int i = 0; i < A::kLoads; ++i) {
+        a.template load<kTail>(i, fill, 0, ap[i], 0, rest);
+        ap[i] += kStep * 2;
+      }
+#pragma unroll
+      for (int i = 0; i < B::kLoads; ++i)
+        b.template load<kTail>(i, fill + A::kBytes, 0, bp, 0, rest);
+      bp += kStep * 2;
+    };
+    auto start = [&](int t) {
+      if (t + 1 < steps || rest == kStep)
+        load(std::false_type{});
+      else
+        load(std::true_type{});
+      fill = after(fill);
+    };
+    for (int t = first; t < first + STAGES - 1 && t < end; ++t) start(t);
+    for (int t = first; t < end; ++t) {
+      if (t + STAGES - 1 <= end)
+        wait_vm<(STAGES - 2) * kLoads>();
+      else
+        wait_vm<0>();
+      wait_lds();  // the step before has been read out of the slot to fill
+      if (t + STAGES - 1 < end) start(t + STAGES - 1);
+      if (t + 1 < steps)
+        multiply<false>(here, nv, rest);
+      else
+        multiply<true>(here, nv, rest);
+      here = after(here);
+    }
+    // the shares, added up in their order
+    static_assert(kRing >= TU * TV * 16 * kWave, "a wave's sums fit its ring");
+    f32x4_t* sums = reinterpret_cast<f32x4_t*>(smem + wave * kRing) + lane_id();
+    wait_lds();
+    if (wave > 0) {
+#pragma unroll
+      for (int u = 0; u < TU; ++u)
+#pragma unroll
+        for (int v = 0; v < TV; ++v) sums[(u * TV + v) * kWave] = acc[u][v];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+    for (int w = 1; w < SPLIT; ++w) {
+      const f32x4_t* other = reinterpret_cast<f32x4_t*>(smem + w * kRing) + lane_id();
+#pragma unroll
+      for (int u = 0; u < TU; ++u)
+#pragma unroll
+        for (int v = 0; v < TV; ++v) acc[u][v] += other[(u * TV + v) * kWave];
+    }
+  }
+
+  __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
+  }
+};
+
+// ---------------------------------------------------------------------------
 // The same for e4m3 operands with a scale per 128 values along r: one step is
 // one block of 128, whose products are summed by one 16 x 16 x 128 matrix
 // instruction per fragment and then scaled in fp32, sx of the token times sw
@@ -569,6 +692,27 @@ matmul_kernel(MatmulParams p, int ntiles) {
   finish<C, ACT>(prod, p, t, wave);
 }
 
+template <class Product, int ACT>
+__global__ void __launch_bounds__(Product::kThreads)
+matmul_stream_kernel(MatmulParams p, int ntiles) {
+  using C = typename Product::C;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n0 = t.n * Columns<C, ACT>::kTile;
+  const uint32_t ld = (uint32_t)p.K * 2;
+  const int rows = min(C::kBv, t.end - t.m0);
+  Product prod;
+  const char* ap[Product::A::kLoads];
+  weight_loads<C, ACT>(prod.a, ap,
+                       static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld, 0, p.F,
+                       p.F - n0, ld);
+  prod.b.init(0, ld, rows);
+  prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, p.K, rows);
+  if (wave == 0) finish<C, ACT>(prod, p, t, 0);
+}
+
 template <class C, int ACT>
 __global__ void __launch_bounds__(C::kThreads)
 matmul_fp8_kernel(MatmulParams p, int ntiles) {
@@ -718,27 +862,36 @@ grad_w_kernel(MatmulGradParams p, const uint16_t* gz, unsigned nt, unsigned pt) 
   }
 }
 
-// 256 x 256 tiles for experts of many rows, 256 x 128 for those of few: a part
-// tile wastes the products of its missing rows.
+// 256 x 256 tiles for experts of many rows, one block to a compute unit; 128 x
+// 128, two blocks to a unit, for the others: the second block works while the
+// first waits for its first loads or stores its results, and a part tile
+// wastes less.  At 4096 x 7168 and 32 experts: 256 rows each 663 us against
+// 685, 128 rows 534 against 493, 64 rows 371 against 346.
 using Large = Config<2, 2, 8, 8>;
-using Small = Config<2, 2, 8, 4>;
-
-// Large tiles where an expert has more rows than one small tile on average
-// and the large tiles alone fill the 256 compute units.
-#ifndef GXL
-#define GXL Large
-#endif
-#ifndef GWL
-#define GWL Large
-#endif
 using Mid = Config<2, 2, 4, 4>;
+// 64 x 16 by four waves that share the steps.
+using Few = StreamProduct<4, 1, 4, 3>;
 // fp8: 128 weight rows by 256 token rows, so that an expert's weights are read
 // once however its 128 or so rows fall.
 using Codes = Config<2, 4, 4, 4>;
 
+constexpr int kUnits = 256;  // compute units
+
+// Large tiles where an expert has more rows than half of one on average and
+// they alone give every compute unit one.
 bool large_tiles(const Segments& s, int u) {
   const int64_t tiles = ((int64_t)s.pairs / Large::kBv) * ((u + Large::kBu - 1) / Large::kBu);
-  return s.pairs / s.E > Small::kBv && tiles >= 256;
+  return s.pairs / s.E > Large::kBv / 2 && tiles >= kUnits;
+}
+
+// The streaming product for up to 4 rows an expert (one token of 8 of 32
+// experts, 4096 x 7168: 82 us against 110 on 128 x 128 tiles; 16 tokens 301
+// against 299), and while those tiles would leave compute units idle, up to
+// 64 (one expert, 64 rows, 2048 x 7168: 21 us against 63).
+bool few_rows(const Segments& s, int u) {
+  const int64_t rows = s.pairs / s.E, busy = s.E < s.pairs ? s.E : s.pairs;
+  if (rows <= 4) return true;
+  return rows <= 64 && busy * ((u + Mid::kBu - 1) / Mid::kBu) < kUnits;
 }
 
 template <class K>
@@ -746,8 +899,6 @@ hipError_t allow_lds(K kernel, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
-
-constexpr int kUnits = 256;  // compute units
 
 template <class C, int ACT>
 hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
@@ -760,6 +911,20 @@ hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p,
                      ntiles);
+  return hipGetLastError();
+}
+
+template <class Product, int ACT>
+hipError_t launch_stream(const MatmulParams& p, hipStream_t st) {
+  using C = typename Product::C;
+  constexpr int kCols = Columns<C, ACT>::kTile;
+  const int ntiles = (p.F + kCols - 1) / kCols;
+  const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  const hipError_t e = allow_lds(matmul_stream_kernel<Product, ACT>, Product::kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((matmul_stream_kernel<Product, ACT>), dim3((unsigned)grid),
+                     dim3(Product::kThreads), Product::kLds, st, p, ntiles);
   return hipGetLastError();
 }
 
@@ -781,7 +946,8 @@ template <int ACT>
 hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
   if (fp8) return launch_codes<Codes, ACT>(p, st);
   if (large_tiles(p.seg, p.P)) return launch_tiles<Large, ACT>(p, st);
-  return launch_tiles<Small, ACT>(p, st);
+  if (few_rows(p.seg, p.P)) return launch_stream<Few, ACT>(p, st);
+  return launch_tiles<Mid, ACT>(p, st);
 }
 
 template <class C>
@@ -860,10 +1026,10 @@ hipError_t launch_expert_matmul_grad(const MatmulGradParams& p, hipStream_t st) 
   const bool large = large_tiles(p.seg, p.K);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.grad_x)
-    e = large ? launch_grad_x<GXL>(p, g, st) : launch_grad_x<Small>(p, g, st);
+    e = large ? launch_grad_x<Large>(p, g, st) : launch_grad_x<Mid>(p, g, st);
   if (e == hipSuccess && p.grad_weight)
-    e = (int64_t)p.K * p.P >= 256 * 256 ? launch_grad_w<GWL>(p, g, st)
-                                        : launch_grad_w<Small>(p, g, st);
+    e = (int64_t)p.K * p.P >= 256 * 256 ? launch_grad_w<Large>(p, g, st)
+                                        : launch_grad_w<Mid>(p, g, st);
   return e;
 }
 
