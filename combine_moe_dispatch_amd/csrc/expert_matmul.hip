@@ -16,6 +16,7 @@
 // a tile of D in registers and walks r in steps of 64: while its four waves
 // multiply one step out of LDS, the loads of the next go straight into the
 // other half of it.
+#include <atomic>
 #include <type_traits>
 
 #include "expert_tile.h"
@@ -394,7 +395,6 @@ struct Fp8Product {
   static_assert(C::kBv == C::kWaves * 32, "a wave brings in the scales of 32 rows");
   static constexpr int kStage = A::kBytes + B::kBytes + kScales;
   static constexpr int kStages = 3, kLds = kStages * kStage;
-  static constexpr int kLoads = A::kLoads + B::kLoads + 1;
   A a;
   B b;
   f32x4_t acc[C::kTu][C::kTv];
@@ -412,13 +412,17 @@ struct Fp8Product {
     return u.v;
   }
 
-  // blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
+  // PART: kTv, or kTv / 2 for a tile whose second half has no rows, which takes
+  // half of B's loads.  blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
   // 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of the weight rows
   // behind the first and the second half of the wave's fragments.  (A plain
   // load of them would wait for every load to LDS before it.)  rows: how many
   // the tile has.
+  template <int PART>
   __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
                                       const char* bp, const float* scale, int blocks, int rows) {
+    constexpr int kRowLoads = B::kLoads * PART / C::kTv;
+    constexpr int kLoads = A::kLoads + kRowLoads + 1;
     ra.init(wave % C::kWu * C::kTu * 16);
     rb.init(wave / C::kWu * 16);
 #pragma unroll
@@ -435,7 +439,7 @@ struct Fp8Product {
         ap[i] += 128;
       }
 #pragma unroll
-      for (int i = 0; i < B::kLoads; ++i)
+      for (int i = 0; i < kRowLoads; ++i)
         b.template load<false>(i, fill + A::kBytes, wave, bp, 0, 0);
       load4_to_lds(fill + A::kBytes + B::kBytes + wave * 256, scale);
       bp += 128;
@@ -470,7 +474,7 @@ struct Fp8Product {
 #pragma unroll
         for (int u = 0; u < C::kTu; ++u) fa[u] = frag(ra, here, u);
 #pragma unroll
-        for (int v = 0; v < C::kTv; ++v) {
+        for (int v = 0; v < PART; ++v) {
           if (v >= nv) break;
           const i32x8_t fb = frag(rb, here + A::kBytes, v * C::kWv);
           const float sx = lds_float(here + sx_at + v * C::kWv / 2 * 256);
@@ -740,7 +744,11 @@ matmul_fp8_kernel(MatmulParams p, int ntiles) {
   const float* scale =
       lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
                 : p.weight_scales + ((size_t)t.e * (p.P / 128) + block + up) * kb;
-  prod.run(smem, wave, ap, static_cast<const char*>(p.x) + (size_t)t.m0 * ld, scale, kb, rows);
+  const char* bp = static_cast<const char*>(p.x) + (size_t)t.m0 * ld;
+  if (rows > C::kBv / 2)
+    prod.template run<C::kTv>(smem, wave, ap, bp, scale, kb, rows);
+  else
+    prod.template run<C::kTv / 2>(smem, wave, ap, bp, scale, kb, rows);
   finish<C, ACT>(prod, p, t, wave);
 }
 
@@ -894,10 +902,19 @@ bool few_rows(const Segments& s, int u) {
   return rows <= 64 && busy * ((u + Mid::kBu - 1) / Mid::kBu) < kUnits;
 }
 
-template <class K>
-hipError_t allow_lds(K kernel, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// More than 64 KB of LDS has to be asked for, once per kernel and device.
+template <auto KERNEL, int BYTES>
+hipError_t allow_lds() {
+  static std::atomic<uint64_t> done{0};
+  int device;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (device & 63);
+  if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <class C, int ACT>
@@ -907,7 +924,7 @@ hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds(matmul_kernel<C, ACT>, kLds);
+  const hipError_t e = allow_lds<matmul_kernel<C, ACT>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p,
                      ntiles);
@@ -921,7 +938,7 @@ hipError_t launch_stream(const MatmulParams& p, hipStream_t st) {
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds(matmul_stream_kernel<Product, ACT>, Product::kLds);
+  const hipError_t e = allow_lds<matmul_stream_kernel<Product, ACT>, Product::kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_stream_kernel<Product, ACT>), dim3((unsigned)grid),
                      dim3(Product::kThreads), Product::kLds, st, p, ntiles);
@@ -935,7 +952,7 @@ hipError_t launch_codes(const MatmulParams& p, hipStream_t st) {
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds(matmul_fp8_kernel<C, ACT>, kLds);
+  const hipError_t e = allow_lds<matmul_fp8_kernel<C, ACT>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_fp8_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds,
                      st, p, ntiles);
@@ -956,7 +973,7 @@ hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStrea
   const int ntiles = (p.K + C::kBu - 1) / C::kBu;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds(grad_x_kernel<C>, kLds);
+  const hipError_t e = allow_lds<grad_x_kernel<C>, kLds>();
   if (e != hipSuccess || grid == 0) return e;
   hipLaunchKernelGGL((grad_x_kernel<C>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p, gz,
                      ntiles);
@@ -969,7 +986,7 @@ hipError_t launch_grad_w(const MatmulGradParams& p, const uint16_t* gz, hipStrea
   const unsigned nt = (p.K + C::kBu - 1) / C::kBu, pt = (p.P + C::kBv - 1) / C::kBv;
   const int64_t tiles = (int64_t)nt * pt * p.seg.E;
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds(grad_w_kernel<C>, kLds);
+  const hipError_t e = allow_lds<grad_w_kernel<C>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((grad_w_kernel<C>), dim3((unsigned)(tiles < kUnits ? tiles : kUnits)),
                      dim3(C::kThreads), kLds, st, p, gz, nt, pt);
