@@ -383,18 +383,18 @@ struct StreamProduct {
 // of the 128 weight rows.  A row of a step is 128 bytes, as in the bf16
 // product, so the tiles in LDS are the same; the chunks of a fragment are
 // taken in an order of their own, equal for both operands, which a sum does
-// not notice.  Eight waves, and three steps in LDS: a serving batch has few
-// rows an expert, so the weights stream through once and the loads in flight
-// count.
+// not notice.  Eight waves, two on every SIMD: one scales while the other
+// multiplies.
 // ---------------------------------------------------------------------------
-template <class C>
+template <class C, int STAGES>
 struct Fp8Product {
   using A = OperandTile<C::kBu, C::kWaves, false, true>;
   using B = OperandTile<C::kBv, C::kWaves, false, false>;
   static constexpr int kScales = C::kWaves * 256;  // one dword a lane
   static_assert(C::kBv == C::kWaves * 32, "a wave brings in the scales of 32 rows");
   static constexpr int kStage = A::kBytes + B::kBytes + kScales;
-  static constexpr int kStages = 3, kLds = kStages * kStage;
+  static constexpr int kLds = STAGES * kStage;
+  static constexpr int kRows = 4;  // of fragments multiplied at a time
   A a;
   B b;
   f32x4_t acc[C::kTu][C::kTv];
@@ -446,8 +446,7 @@ struct Fp8Product {
       scale += 1;
       fill = after(fill);
     };
-    start();
-    if (blocks > 1) start();
+    for (int t = 0; t < STAGES - 1 && t < blocks; ++t) start();
     // the fragments of this wave that hold rows at all
     const int wv = wave / C::kWu;
     const int nv = min((rows - wv * 16 + C::kWv * 16 - 1) / (C::kWv * 16), C::kTv);
@@ -460,34 +459,38 @@ struct Fp8Product {
       return *(const __attribute__((address_space(3))) float*)(uintptr_t)p;
     };
     for (int t = 0; t < blocks; ++t) {
-      if (t + 1 < blocks)
-        wait_vm<kLoads>();
+      if (t + STAGES - 1 <= blocks)
+        wait_vm<(STAGES - 2) * kLoads>();
       else
         wait_vm<0>();
       wait_lds();  // this wave has read the step before out
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      if (t + 2 < blocks) start();
+      if (t + STAGES - 1 < blocks) start();
       if (nv > 0) {
         const float sw[2] = {lds_float(here + sw_at), lds_float(here + sw_at + 4)};
-        i32x8_t fa[C::kTu];
 #pragma unroll
-        for (int u = 0; u < C::kTu; ++u) fa[u] = frag(ra, here, u);
+        for (int u0 = 0; u0 < C::kTu; u0 += kRows) {
+          i32x8_t fa[kRows];
 #pragma unroll
-        for (int v = 0; v < PART; ++v) {
-          if (v >= nv) break;
-          const i32x8_t fb = frag(rb, here + A::kBytes, v * C::kWv);
-          const float sx = lds_float(here + sx_at + v * C::kWv / 2 * 256);
-          f32x4_t part[C::kTu];
+          for (int u = 0; u < kRows; ++u) fa[u] = frag(ra, here, u0 + u);
 #pragma unroll
-          for (int u = 0; u < C::kTu; ++u)
-            part[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[u], fb, f32x4_t{}, 0, 0,
-                                                                       0, 0, 0, 0);
+          for (int v = 0; v < PART; ++v) {
+            if (v >= nv) break;
+            const i32x8_t fb = frag(rb, here + A::kBytes, v * C::kWv);
+            const float sx = lds_float(here + sx_at + v * C::kWv / 2 * 256);
+            f32x4_t part[kRows];
 #pragma unroll
-          for (int u = 0; u < C::kTu; ++u) {
-            const float s = sx * sw[u < C::kTu / 2 ? 0 : 1];
+            for (int u = 0; u < kRows; ++u)
+              part[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[u], fb, f32x4_t{}, 0,
+                                                                         0, 0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[u][v][i] = fmaf(part[u][i], s, acc[u][v][i]);
+            for (int u = 0; u < kRows; ++u) {
+              const float s = sx * sw[u0 + u < C::kTu / 2 ? 0 : 1];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[u0 + u][v][i] = fmaf(part[u][i], s, acc[u0 + u][v][i]);
+            }
           }
         }
       }
@@ -717,10 +720,10 @@ matmul_stream_kernel(MatmulParams p, int ntiles) {
   if (wave == 0) finish<C, ACT>(prod, p, t, 0);
 }
 
-template <class C, int ACT>
+template <class C, int STAGES, int ACT>
 __global__ void __launch_bounds__(C::kThreads)
 matmul_fp8_kernel(MatmulParams p, int ntiles) {
-  using Product = Fp8Product<C>;
+  using Product = Fp8Product<C, STAGES>;
   using Cols = Columns<C, ACT>;
   extern __shared__ __align__(1024) char smem[];
   Tile t;
@@ -879,9 +882,12 @@ using Large = Config<2, 2, 8, 8>;
 using Mid = Config<2, 2, 4, 4>;
 // 64 x 16 by four waves that share the steps.
 using Few = StreamProduct<4, 1, 4, 3>;
-// fp8: 128 weight rows by 256 token rows, so that an expert's weights are read
-// once however its 128 or so rows fall.
-using Codes = Config<2, 4, 4, 4>;
+// fp8, 256 token rows by 256 weight rows in two steps of LDS or by 128 in
+// three: the large tile moves less per product (32 experts of 4096 x 7168: 512
+// rows each 444 us against 527, 128 rows 236 against 284), the small one has
+// twice the blocks and the deeper ring for few rows (64 rows 201 against 195).
+using Codes = Config<2, 4, 8, 4>;
+using FewCodes = Config<2, 4, 4, 4>;
 
 constexpr int kUnits = 256;  // compute units
 
@@ -890,6 +896,15 @@ constexpr int kUnits = 256;  // compute units
 bool large_tiles(const Segments& s, int u) {
   const int64_t tiles = ((int64_t)s.pairs / Large::kBv) * ((u + Large::kBu - 1) / Large::kBu);
   return s.pairs / s.E > Large::kBv / 2 && tiles >= kUnits;
+}
+
+// The large fp8 tile where an expert has more than a quarter of its rows on
+// average and every compute unit gets one.
+bool large_codes(const Segments& s, int u) {
+  const int64_t rows = s.pairs / s.E, busy = s.E < s.pairs ? s.E : s.pairs;
+  const int64_t tiles = busy * ((rows + Codes::kBv - 1) / Codes::kBv) *
+                        ((u + Codes::kBu - 1) / Codes::kBu);
+  return rows > Codes::kBv / 4 && tiles >= kUnits;
 }
 
 // The streaming product for up to 4 rows an expert (one token of 8 of 32
@@ -945,23 +960,26 @@ hipError_t launch_stream(const MatmulParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <class C, int ACT>
+template <class C, int STAGES, int ACT>
 hipError_t launch_codes(const MatmulParams& p, hipStream_t st) {
   constexpr int kCols = Columns<C, ACT>::kTile;
-  constexpr int kLds = Fp8Product<C>::kLds;
+  constexpr int kLds = Fp8Product<C, STAGES>::kLds;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = allow_lds<matmul_fp8_kernel<C, ACT>, kLds>();
+  const hipError_t e = allow_lds<matmul_fp8_kernel<C, STAGES, ACT>, kLds>();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((matmul_fp8_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds,
+  hipLaunchKernelGGL((matmul_fp8_kernel<C, STAGES, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds,
                      st, p, ntiles);
   return hipGetLastError();
 }
 
 template <int ACT>
 hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
-  if (fp8) return launch_codes<Codes, ACT>(p, st);
+  if (fp8) {
+    if (large_codes(p.seg, p.P)) return launch_codes<Codes, 2, ACT>(p, st);
+    return launch_codes<FewCodes, 3, ACT>(p, st);
+  }
   if (large_tiles(p.seg, p.P)) return launch_tiles<Large, ACT>(p, st);
   if (few_rows(p.seg, p.P)) return launch_stream<Few, ACT>(p, st);
   return launch_tiles<Mid, ACT>(p, st);

@@ -96,6 +96,9 @@ def test_optional_arguments(name, bias, residual, pre):
     ("swiglu", 200, 2, 1, 2, 90, 256, 256),
     ("none", 600, 3, 2, 1, 0, 512, 640),
     ("swiglu", 600, 3, 2, 1, 0, 384, 384),
+    ("swiglu", 2100, 1, 1, 1, 0, 128, 4096),  # enough rows and columns for the largest tiles
+    ("none", 1100, 2, 1, 1, 0, 256, 8320),
+    ("silu", 1500, 5, 2, 1, 0, 128, 3456),
 ])
 def test_fp8(name, T, E, k, N, C, K, F):
     run(T, E, k, N, C, K, F, name, fp8=True)
