@@ -10,7 +10,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool rows_ok(const void* p) { return p && aligned16(p); }
 bool maybe_rows_ok(const void* p) { return aligned16(p); }
 
-moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+moe_status from_hip(hipError_t e) {
+  if (e == hipErrorNotSupported) return MOE_ERR_UNSUPPORTED;  // the launchers' own limits
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
 
 // A shape's receive rows.  For a bad shape the combine's second half, which
 // checks the shape before anything else and finds nothing to launch, names
@@ -28,7 +31,8 @@ moe_status check_linear(const moe_shape* s, const moe_linear* l, int* P) {
   const int unit = s->payload == MOE_PAYLOAD_FP8_E4M3_B128 ? 128 : 8;
   if (l->in_features % unit != 0 || l->out_features % unit != 0) return MOE_ERR_INVALID_ARG;
   const int64_t p = (l->activation == MOE_ACT_SWIGLU ? 2 : 1) * (int64_t)l->out_features;
-  if (p > INT32_MAX / 4 || l->in_features > INT32_MAX / 4) return MOE_ERR_UNSUPPORTED;
+  // a tile's rows are addressed with 32-bit byte offsets
+  if (p > MOE_MAX_FEATURES || l->in_features > MOE_MAX_FEATURES) return MOE_ERR_UNSUPPORTED;
   *P = (int)p;
   return MOE_OK;
 }

@@ -938,7 +938,7 @@ hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
   constexpr int kLds = TileProduct<C, false, false>::kLds;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > INT32_MAX) return hipErrorNotSupported;
   const hipError_t e = allow_lds<matmul_kernel<C, ACT>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p,
@@ -952,7 +952,7 @@ hipError_t launch_stream(const MatmulParams& p, hipStream_t st) {
   constexpr int kCols = Columns<C, ACT>::kTile;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > INT32_MAX) return hipErrorNotSupported;
   const hipError_t e = allow_lds<matmul_stream_kernel<Product, ACT>, Product::kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_stream_kernel<Product, ACT>), dim3((unsigned)grid),
@@ -966,7 +966,7 @@ hipError_t launch_codes(const MatmulParams& p, hipStream_t st) {
   constexpr int kLds = Fp8Product<C, STAGES>::kLds;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > INT32_MAX) return hipErrorNotSupported;
   const hipError_t e = allow_lds<matmul_fp8_kernel<C, STAGES, ACT>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_fp8_kernel<C, STAGES, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds,
@@ -990,7 +990,7 @@ hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStrea
   constexpr int kLds = TileProduct<C, true, false>::kLds;
   const int ntiles = (p.K + C::kBu - 1) / C::kBu;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > INT32_MAX) return hipErrorNotSupported;
   const hipError_t e = allow_lds<grad_x_kernel<C>, kLds>();
   if (e != hipSuccess || grid == 0) return e;
   hipLaunchKernelGGL((grad_x_kernel<C>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p, gz,
@@ -1003,7 +1003,7 @@ hipError_t launch_grad_w(const MatmulGradParams& p, const uint16_t* gz, hipStrea
   constexpr int kLds = TileProduct<C, true, true>::kLds + kTableBytes;
   const unsigned nt = (p.K + C::kBu - 1) / C::kBu, pt = (p.P + C::kBv - 1) / C::kBv;
   const int64_t tiles = (int64_t)nt * pt * p.seg.E;
-  if (tiles > INT32_MAX) return hipErrorInvalidValue;
+  if (tiles > INT32_MAX) return hipErrorNotSupported;
   const hipError_t e = allow_lds<grad_w_kernel<C>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((grad_w_kernel<C>), dim3((unsigned)(tiles < kUnits ? tiles : kUnits)),

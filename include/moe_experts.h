@@ -34,9 +34,11 @@ typedef enum {
   MOE_ACT_SWIGLU = 3
 } moe_activation;
 
+#define MOE_MAX_FEATURES (1 << 22)
+
 /* One linear layer held by every expert (host struct, read during the call).
  * P below is the number of columns before the activation: 2 * out_features for
- * MOE_ACT_SWIGLU, else out_features. */
+ * MOE_ACT_SWIGLU, else out_features.  Neither K nor P exceeds MOE_MAX_FEATURES. */
 typedef struct {
   int32_t in_features;  /* K > 0: K % 8 == 0; fp8 payload: K % 128 == 0 */
   int32_t out_features; /* F > 0: F % 8 == 0; fp8 payload: F % 128 == 0 */
@@ -69,8 +71,8 @@ typedef struct {
  *   pre           [rows][P] bf16 out, bf16(z), for the backward pass; or NULL.
  * Sums are fp32; with fp8 the products of each 128 columns are summed first
  * and then scaled.  Rows of no segment are neither read for a result nor
- * written.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (E, k or rows
- * past the library's limits, or 2^31 - 1 or more tiles).
+ * written.  Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED for E, k, rows
+ * or features past the library's limits.
  */
 moe_status moe_expert_matmul(const moe_shape *shape, const moe_linear *linear, const void *x,
                              const float *x_scales, const moe_layout *layout,

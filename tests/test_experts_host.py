@@ -83,6 +83,8 @@ def test_matmul_refusals():
     assert matmul(shape=fp8, lin=(64, 128, 0), xs=A, ws=A) == INVALID
     assert matmul(shape=fp8, lin=(128, 64, 0), xs=A, ws=A) == INVALID
     assert matmul(lin=(64, 1 << 30, 3)) == UNSUPPORTED
+    assert matmul(lin=((1 << 22) + 8, 32, 0)) == UNSUPPORTED
+    assert matmul(lin=(64, (1 << 21) + 8, 3)) == UNSUPPORTED
     assert matmul(shape=(0, 64, 8, 2, 2, 0, 0), x=None, w=None, y=None) == 0  # nothing to do
 
 

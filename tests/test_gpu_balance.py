@@ -245,3 +245,30 @@ def test_large_batch_is_deterministic():
     assert torch.equal(first[3].cpu().long(),
                        ref.balance(torch.zeros(20000, 256, dtype=torch.float64), ids, 1,
                                    off.tolist(), COEF)[3])
+
+
+@pytest.mark.parametrize("E", [64, 256, 384, 1024])
+def test_misaligned_arrays(E):
+    """Logits, bias, counts and outputs four bytes past a 16-byte boundary: the same values."""
+    T, k = 200, 3
+    l, b, ids, off, w, gw = make(T, E, k, 1, True, [0, 90, 200], False, 3)
+
+    def odd(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        flat[1:].copy_(t.flatten())
+        return flat[1:].view(t.shape)
+
+    want = api.moe_balance_loss(c(l), c(b), c(ids), 1, COEF, c(off))
+    got = api.moe_balance_loss(odd(l), odd(b), odd(ids), 1, COEF, odd(off))
+    # the order of a row's sum differs, so fp32 sums of E terms and their mean
+    assert torch.equal(got[1], want[1]) and torch.equal(got[3], want[3])
+    rel = (2 * E + T) * ref.U32
+    assert ((got[2] - want[2]).abs() <= rel * want[2]).all()
+    kw = dict(coef=COEF, expert_counts=want[1], seq_tokens=want[3])
+    a, _ = api.moe_route_backward(c(l), c(b), c(ids), c(w), c(gw), 1, seq_offsets=c(off), **kw)
+    out = odd(torch.zeros(T, E))
+    d, _ = api.moe_route_backward(odd(l), odd(b), c(ids), odd(w), odd(gw), 1, seq_offsets=c(off),
+                                  grad_logits=out, **kw)
+    size = magnitude(l, b, ids, off, 1, w, gw, want[1].cpu(), want[3].cpu())
+    assert d is out
+    assert ((a - d).abs().cpu().double() <= 2 * rel * size / 0.75 + ref.TINY).all()
