@@ -56,10 +56,17 @@ __device__ __forceinline__ void add8(float (&v)[8], const float* p) {
 
 __device__ __forceinline__ float sigmoid_f32(float v) { return 1.0f / (1.0f + expf(-v)); }
 
+// The same for results that are rounded to bf16 next: the hardware's 2^x and
+// reciprocal, off by (1 + |v|) 2^-23 of the value or so where the rounding is
+// off by 2^-8.  A tile's activations are thousands of these per lane.
+__device__ __forceinline__ float sigmoid_short(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
+}
+
 // act(z) for the one-input activations
 template <int ACT>
 __device__ __forceinline__ float act_f32(float z) {
-  if (ACT == kActSilu) return z * sigmoid_f32(z);
+  if (ACT == kActSilu) return z * sigmoid_short(z);
   if (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
   return z;
 }

@@ -649,20 +649,26 @@ __device__ __forceinline__ void finish(const Product& prod, const MatmulParams& 
   using Cols = Columns<C, ACT>;
   const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
 #pragma unroll
-  for (int v = 0; v < C::kTv; ++v) {
-    const int m = t.m0 + (v * C::kWv + wv) * 16 + (lane & 15);
-    if (m >= t.end) continue;
+  for (int a = 0; a < Cols::kPairs; ++a) {
+    const int col = t.n * Cols::kTile + wu * Cols::kWave + a * 32 + (lane >> 4) * 8;
+    if (col >= p.F) continue;
+    float bias[8] = {}, bias_up[8] = {};  // once for all rows
+    if (p.bias) {
+      const float* b = p.bias + (size_t)t.e * p.P + col;
+      add8(bias, b);
+      if (Cols::kGated) add8(bias_up, b + p.F);
+    }
 #pragma unroll
-    for (int a = 0; a < Cols::kPairs; ++a) {
-      const int col = t.n * Cols::kTile + wu * Cols::kWave + a * 32 + (lane >> 4) * 8;
-      if (col >= p.F) continue;
+    for (int v = 0; v < C::kTv; ++v) {
+      const int m = t.m0 + (v * C::kWv + wv) * 16 + (lane & 15);
+      if (m >= t.end) continue;
       float z[8], up[8];
       prod.eight(z, a, v);
       if (Cols::kGated) prod.eight(up, a + Cols::kPairs, v);
-      if (p.bias) {
-        const float* b = p.bias + (size_t)t.e * p.P + col;
-        add8(z, b);
-        if (Cols::kGated) add8(up, b + p.F);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z[i] += bias[i];
+        if (Cols::kGated) up[i] += bias_up[i];
       }
       if (p.pre) {
         store8(p.pre + (size_t)m * p.P + col, z);
@@ -670,7 +676,7 @@ __device__ __forceinline__ void finish(const Product& prod, const MatmulParams& 
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        z[i] = Cols::kGated ? z[i] * sigmoid_f32(z[i]) * up[i] : act_f32<ACT>(z[i]);
+        z[i] = Cols::kGated ? z[i] * sigmoid_short(z[i]) * up[i] : act_f32<ACT>(z[i]);
       const size_t at = (size_t)m * p.F + col;
       if (p.residual) add8(z, p.residual + at);
       store8(p.y + at, z);

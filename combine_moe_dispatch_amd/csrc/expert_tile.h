@@ -22,26 +22,27 @@ constexpr int kGroupRows = 4;
 
 // Tile `b` of the launch, or false when there are fewer.  Every wave works it
 // out for itself: lane i of a pass looks at expert base + i, and a prefix sum
-// over the lanes finds the expert whose tiles hold it.
+// over the lanes finds the expert whose tiles hold it.  The first pass counts
+// all tiles, so that they can be dealt to the XCDs in runs; up to 64 experts
+// it is the only one.
 template <int BV>
 __device__ __forceinline__ bool find_tile(const Segments& s, int ntiles, unsigned b, Tile& t) {
   const int lane = lane_id();
-  // all tiles, so that the tiles can be dealt to the XCDs in runs
-  unsigned total = 0;
-  for (int base = 0; base < s.E; base += kWave) {
-    int begin = 0, end = 0;
+  int begin, end, mt, incl;
+  auto look = [&](int base) {
+    begin = end = 0;
     if (base + lane < s.E) segment_of(s, base + lane, begin, end);
-    const int mt = end > begin ? (end - begin + BV - 1) / BV : 0;
-    total += (unsigned)__builtin_amdgcn_readlane(wave_inclusive_sum_dpp(mt), 63);
-  }
+    mt = end > begin ? (end - begin + BV - 1) / BV : 0;
+    incl = wave_inclusive_sum_dpp(mt);
+    return (unsigned)__builtin_amdgcn_readlane(incl, 63);
+  };
+  unsigned total = look(0);
+  for (int base = kWave; base < s.E; base += kWave) total += look(base);
   total *= (unsigned)ntiles;
   if (b >= total) return false;
   unsigned left = xcd_local_block(b, total);
   for (int base = 0; base < s.E; base += kWave) {
-    int begin = 0, end = 0;
-    if (base + lane < s.E) segment_of(s, base + lane, begin, end);
-    const int mt = end > begin ? (end - begin + BV - 1) / BV : 0;
-    const int incl = wave_inclusive_sum_dpp(mt);
+    if (s.E > kWave) look(base);
     const unsigned here = (unsigned)__builtin_amdgcn_readlane(incl, 63) * (unsigned)ntiles;
     if (left >= here) {
       left -= here;
