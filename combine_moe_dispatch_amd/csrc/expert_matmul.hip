@@ -56,9 +56,9 @@ struct TileProduct {
   typename A::template Reader<C::kTu> ra;
   typename B::template Reader<C::kTv> rb;
 
-  // A tile whose second half has no rows (only where B's rows run along r) takes
-  // half of the products and of B's loads: PART is how much of the fragments
-  // along v a wave has to do, kTv or kTv / 2.
+  // A tile whose last quarters have no rows (only where B's rows run along r)
+  // leaves out their products and B's loads of them: PART is how many of the
+  // fragments along v a wave has to do, in quarters of kTv.
   template <int PART>
   static constexpr int kPartLoads = A::kLoads + B::kLoads * PART / C::kTv;
 
@@ -234,15 +234,21 @@ struct TileProduct {
   }
 
   // A tile of `rows` along v, from its first load on.
-  __device__ __forceinline__ void begin_and_run(int rows) {
+  template <int PART>
+  __device__ __forceinline__ void begin_and_run() {
     static_assert(!BT, "the front of a transposed operand's tile is not its first columns");
-    if (rows > C::kBv / 2) {
-      begin<C::kTv>();
-      run<C::kTv>(0);
-    } else {
-      begin<C::kTv / 2>();
-      run<C::kTv / 2>(0);
-    }
+    begin<PART>();
+    run<PART>(0);
+  }
+  __device__ __forceinline__ void begin_and_run(int rows) {
+    if (rows > C::kBv * 3 / 4)
+      begin_and_run<C::kTv>();
+    else if (rows > C::kBv / 2)
+      begin_and_run<C::kTv * 3 / 4>();
+    else if (rows > C::kBv / 4)
+      begin_and_run<C::kTv / 2>();
+    else
+      begin_and_run<C::kTv / 4>();
   }
 
   // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours
@@ -412,8 +418,7 @@ struct Fp8Product {
     return u.v;
   }
 
-  // PART: kTv, or kTv / 2 for a tile whose second half has no rows, which takes
-  // half of B's loads.  blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
+  // PART: as in TileProduct.  blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
   // 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of the weight rows
   // behind the first and the second half of the wave's fragments.  (A plain
   // load of them would wait for every load to LDS before it.)  rows: how many
@@ -754,10 +759,14 @@ matmul_fp8_kernel(MatmulParams p, int ntiles) {
       lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
                 : p.weight_scales + ((size_t)t.e * (p.P / 128) + block + up) * kb;
   const char* bp = static_cast<const char*>(p.x) + (size_t)t.m0 * ld;
-  if (rows > C::kBv / 2)
+  if (rows > C::kBv * 3 / 4)
     prod.template run<C::kTv>(smem, wave, ap, bp, scale, kb, rows);
-  else
+  else if (rows > C::kBv / 2)
+    prod.template run<C::kTv * 3 / 4>(smem, wave, ap, bp, scale, kb, rows);
+  else if (rows > C::kBv / 4)
     prod.template run<C::kTv / 2>(smem, wave, ap, bp, scale, kb, rows);
+  else
+    prod.template run<C::kTv / 4>(smem, wave, ap, bp, scale, kb, rows);
   finish<C, ACT>(prod, p, t, wave);
 }
 

@@ -13,11 +13,14 @@ ACT = {"none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 FILL = -7.0  # what outputs hold before a call
 
 
-def layout(T, E, k, N, C, K, seed, hot=None, bad=False, fp8=False):
-    """Rows dispatched by the library into a poisoned receive buffer."""
+def layout(T, E, k, N, C, K, seed, hot=None, bad=False, fp8=False, counts=None):
+    """Rows dispatched by the library into a poisoned receive buffer.  counts:
+    rows of each expert (k == 1)."""
     shape = api.Shape(T, K, E, k, N, C, 1 if fp8 else 0)
     ids = inputs.random_ids(T, k, E, seed, distinct=k <= E, hot=hot)
     ids = torch.from_numpy(ids).cuda()
+    if counts is not None:
+        ids = torch.repeat_interleave(torch.arange(E), torch.tensor(counts)).int().cuda().view(T, 1)
     if bad:
         ids[::3, 0] = E
         ids[1::5] = -1
@@ -308,6 +311,37 @@ def test_gradients_of_wide_inputs(name, T, E, K, F):
     api.moe_expert_matmul_backward(shape, lin, gy, recv, lay, w, z, gx, gw, gb,
                                    api.alloc_expert_workspace(shape, lin, "cuda"))
     want, tol = ref.matmul_grad(host(gy), host(recv), host(w), host(pre), spans, name)
+    for got, wanted, bound, what in zip((gx.view(torch.bfloat16), gw, gb), want, tol,
+                                        ("grad_x", "grad_weight", "grad_bias")):
+        ref.check(got, wanted, bound, what)
+
+
+@pytest.mark.parametrize("counts,F,fp8", [
+    ([296, 356, 426, 490], 11264, False),      # last tiles of 40, 100, 170, 234 of 256 rows
+    ([138, 178, 210, 250, 0], 264, False),     # of 10, 50, 82, 122 of 128
+    ([296, 356, 426, 490], 8192, True),
+    ([20, 90, 60, 1], 384, True),
+])
+def test_part_tiles(counts, F, fp8):
+    """Every quarter of a tile that the last rows of an expert may reach into."""
+    T, E = sum(counts), len(counts)
+    K = 128 if fp8 else 72
+    run(T, E, 1, 1, 0, K, F, "none", fp8=fp8, counts=counts, seed=T)
+    run(T, E, 1, 1, 0, K, F // 2, "swiglu", fp8=fp8, counts=counts, seed=T)
+
+
+@pytest.mark.parametrize("counts,K", [([296, 356, 426, 490], 11264), ([138, 178, 0, 210, 250], 264)])
+def test_part_tiles_of_gradients(counts, K):
+    T, E, F = sum(counts), len(counts), 72
+    shape, lay, recv, _, spans = layout(T, E, 1, 1, 0, K, T, counts=counts)
+    w, _ = weights(E, F, K, T, False)
+    gen = torch.Generator().manual_seed(T)
+    gy = torch.randn(T, F, generator=gen).bfloat16().cuda()
+    gx, gw, gb = torch.empty_like(recv), torch.empty_like(w), torch.empty(E, F, device="cuda")
+    lin = api.Linear(K, F)
+    api.moe_expert_matmul_backward(shape, lin, gy, recv, lay, w, None, gx, gw, gb,
+                                   api.alloc_expert_workspace(shape, lin, "cuda"))
+    want, tol = ref.matmul_grad(host(gy), host(recv), host(w), None, spans, "none")
     for got, wanted, bound, what in zip((gx.view(torch.bfloat16), gw, gb), want, tol,
                                         ("grad_x", "grad_weight", "grad_bias")):
         ref.check(got, wanted, bound, what)
