@@ -318,9 +318,9 @@ def test_gradients_of_wide_inputs(name, T, E, K, F):
 
 @pytest.mark.parametrize("counts,F,fp8", [
     ([296, 356, 426, 490], 11264, False),      # last tiles of 40, 100, 170, 234 of 256 rows
-    ([138, 178, 210, 250, 0], 264, False),     # of 10, 50, 82, 122 of 128
+    ([138, 178, 210, 250, 0], 272, False),     # of 10, 50, 82, 122 of 128
     ([296, 356, 426, 490], 8192, True),
-    ([20, 90, 60, 1], 384, True),
+    ([20, 90, 60, 1], 512, True),
 ])
 def test_part_tiles(counts, F, fp8):
     """Every quarter of a tile that the last rows of an expert may reach into."""
