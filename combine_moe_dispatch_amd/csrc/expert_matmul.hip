@@ -890,9 +890,9 @@ grad_w_kernel(MatmulGradParams p, const uint16_t* gz, unsigned nt, unsigned pt) 
 
 // 256 x 256 tiles for experts of many rows, one block to a compute unit; 128 x
 // 128, two blocks to a unit, for the others: the second block works while the
-// first waits for its first loads or stores its results, and a part tile
-// wastes less.  At 4096 x 7168 and 32 experts: 256 rows each 663 us against
-// 685, 128 rows 534 against 493, 64 rows 371 against 346.
+// first waits for its first loads or stores its results (256 x 128 tiles, one
+// to a unit, took 371 us against 346 at 64 rows an expert, 32 experts of 4096
+// x 7168, and 42 us against 37 for 1021 rows of one expert of 7168 x 2048).
 using Large = Config<2, 2, 8, 8>;
 using Mid = Config<2, 2, 4, 4>;
 // 64 x 16 by four waves that share the steps.
@@ -906,20 +906,25 @@ using FewCodes = Config<2, 4, 4, 4>;
 
 constexpr int kUnits = 256;  // compute units
 
-// Large tiles where an expert has more rows than half of one on average and
-// they alone give every compute unit one.
+int64_t tiles_of(const Segments& s, int u, int bu, int bv) {
+  const int64_t rows = s.pairs / s.E, busy = s.E < s.pairs ? s.E : s.pairs;
+  return busy * ((rows + bv - 1) / bv) * ((u + bu - 1) / bu);
+}
+
+// Large tiles from 112 rows an expert on, where some experts begin to need two
+// small ones (32 experts, 4096 x 7168: 96 rows 394 us against 357 on small
+// tiles, 128 rows 435 against 501, 256 rows 637 against 668, 512 rows 905
+// against 1024), if they give three quarters of the compute units one (one
+// expert, 7168 x 2048: 112 tiles 59 us against 36, 168 tiles 61 against 59, 196
+// tiles 63 against 66).
 bool large_tiles(const Segments& s, int u) {
-  const int64_t tiles = ((int64_t)s.pairs / Large::kBv) * ((u + Large::kBu - 1) / Large::kBu);
-  return s.pairs / s.E > Large::kBv / 2 && tiles >= kUnits;
+  return s.pairs / s.E >= 112 && tiles_of(s, u, Large::kBu, Large::kBv) >= kUnits * 3 / 4;
 }
 
 // The large fp8 tile where an expert has more than a quarter of its rows on
 // average and every compute unit gets one.
 bool large_codes(const Segments& s, int u) {
-  const int64_t rows = s.pairs / s.E, busy = s.E < s.pairs ? s.E : s.pairs;
-  const int64_t tiles = busy * ((rows + Codes::kBv - 1) / Codes::kBv) *
-                        ((u + Codes::kBu - 1) / Codes::kBu);
-  return rows > Codes::kBv / 4 && tiles >= kUnits;
+  return s.pairs / s.E > Codes::kBv / 4 && tiles_of(s, u, Codes::kBu, Codes::kBv) >= kUnits;
 }
 
 // The streaming product for up to 4 rows an expert (one token of 8 of 32
@@ -927,9 +932,8 @@ bool large_codes(const Segments& s, int u) {
 // against 299), and while those tiles would leave compute units idle, up to
 // 64 (one expert, 64 rows, 2048 x 7168: 21 us against 63).
 bool few_rows(const Segments& s, int u) {
-  const int64_t rows = s.pairs / s.E, busy = s.E < s.pairs ? s.E : s.pairs;
-  if (rows <= 4) return true;
-  return rows <= 64 && busy * ((u + Mid::kBu - 1) / Mid::kBu) < kUnits;
+  const int64_t rows = s.pairs / s.E;
+  return rows <= 4 || (rows <= 64 && tiles_of(s, u, Mid::kBu, Mid::kBv) < kUnits);
 }
 
 // More than 64 KB of LDS has to be asked for, once per kernel and device.

@@ -345,3 +345,24 @@ def test_part_tiles_of_gradients(counts, K):
     for got, wanted, bound, what in zip((gx.view(torch.bfloat16), gw, gb), want, tol,
                                         ("grad_x", "grad_weight", "grad_bias")):
         ref.check(got, wanted, bound, what)
+
+
+@pytest.mark.parametrize("T,E,k", [(100, 200, 4), (9, 1024, 3), (900, 70, 8), (1, 65, 2)])
+def test_many_experts(T, E, k):
+    """More experts than a wave has lanes, most of them with few rows or none."""
+    run(T, E, k, 1, 0, 40, 24, "swiglu", seed=E)
+    if E < 1000:
+        run(T, E, k, 5 if E % 5 == 0 else 1, 0, 128, 128, "none", fp8=True, seed=E)
+    K, F = 40, 24
+    shape, lay, recv, _, spans = layout(T, E, k, 1, 0, K, E)
+    w, _ = weights(E, F, K, E, False)
+    gen = torch.Generator().manual_seed(E)
+    gy = torch.randn(T * k, F, generator=gen).bfloat16().cuda()
+    gx, gw, gb = torch.empty_like(recv), torch.empty_like(w), torch.empty(E, F, device="cuda")
+    lin = api.Linear(K, F)
+    api.moe_expert_matmul_backward(shape, lin, gy, recv, lay, w, None, gx, gw, gb,
+                                   api.alloc_expert_workspace(shape, lin, "cuda"))
+    want, tol = ref.matmul_grad(host(gy), host(recv), host(w), None, spans, "none")
+    for got, wanted, bound, what in zip((gx.view(torch.bfloat16), gw, gb), want, tol,
+                                        ("grad_x", "grad_weight", "grad_bias")):
+        ref.check(got, wanted, bound, what)
