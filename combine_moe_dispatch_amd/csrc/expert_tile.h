@@ -115,6 +115,12 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 __device__ __forceinline__ void mfma_in_place(f32x4_t& c, bf16x8_t a, bf16x8_t b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
+// A matrix instruction may not read what a vector instruction wrote less than
+// two wait states before; mfma_in_place keeps no such distance by itself.  Its
+// operands come out of LDS, whose reads are waited for, except where they are
+// masked: those pass through here.  (The two states in front of every product
+// take 1% of a prefill's time.)
+__device__ __forceinline__ void operand_written(bf16x8_t& v) { asm volatile("s_nop 1" : "+v"(v)); }
 // The last product's results get written (8 passes of 4 cycles).
 __device__ __forceinline__ void mfma_results() { asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15"); }
 __device__ __forceinline__ void mfma_result(f32x4_t& c) { asm volatile("" : "+a"(c)); }
@@ -250,6 +256,7 @@ struct OperandTile {
           const uint32_t hi = r + 2 * j + 1 < left ? 0xffff0000u : 0u;
           u.w[j] &= lo | hi;
         }
+        operand_written(u.v);
       }
       return u.v;
     }
