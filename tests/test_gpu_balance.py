@@ -272,3 +272,66 @@ def test_misaligned_arrays(E):
     size = magnitude(l, b, ids, off, 1, w, gw, want[1].cpu(), want[3].cpu())
     assert d is out
     assert ((a - d).abs().cpu().double() <= 2 * rel * size / 0.75 + ref.TINY).all()
+
+
+@pytest.mark.parametrize("T,first,run", [(30, 11, 100000), (500, 16, 300000), (500, 250, 7), (0, 0, 50)])
+def test_long_runs_of_empty_sequences(T, first, run):
+    """Empty sequences between two others, more than there are tokens: the same
+    values as without them."""
+    l, b, ids, _, w, gw = make(T, 40, 3, 1, True, None, False, 4)
+    short = torch.tensor([0, first, T], dtype=torch.int32)
+    long = torch.tensor([0] + [first] * (run + 1) + [T], dtype=torch.int32)
+    S, at = run + 2, [0, run + 1]
+    loss, counts, probs, tokens = forward(l, b, ids, short, 1)
+    got = forward(l, b, ids, long, 1)
+    assert torch.equal(got[1][at], counts) and torch.equal(got[3][at], tokens)
+    # the same sums over at most 500 tokens, perhaps in another order
+    bound = 1024 * ref.U32
+    assert ((got[2][at] - probs).abs() <= bound * probs).all()
+    for t in got[1:]:
+        assert (t[1:-1] == 0).all()
+    assert abs(float(got[0]) * S - 2 * float(loss)) <= 2 * bound * 2 * float(loss)
+    kw = dict(expert_counts=counts, seq_tokens=tokens)
+    want, _ = api.moe_route_backward(c(l), c(b), c(ids), c(w), c(gw), 1, coef=COEF,
+                                     seq_offsets=c(short), **kw)
+    kw = dict(expert_counts=got[1], seq_tokens=got[3])
+    grad, _ = api.moe_route_backward(c(l), c(b), c(ids), c(w), c(gw), 1, coef=COEF * S / 2,
+                                     seq_offsets=c(long), **kw)
+    # the factor coef / S is rounded in another place: a few roundings of each part,
+    # which are at most the balance part (E/k coef / n) and the routed one in size
+    size = 2 * 40 / 3 * COEF / max(min(first, T - first), 1) + gw.abs().amax(1, keepdim=True) \
+        if T else torch.zeros(0, 1)
+    assert ((grad - want).abs().cpu() <= 16 * ref.U32 * size).all()
+
+
+@pytest.mark.parametrize("T", [1, 64, 65])
+@pytest.mark.parametrize("S", [3, 4, 5, 64, 200])
+def test_few_tokens_in_many_sequences(T, S):
+    offsets = [min(i * T // S, T) for i in range(S)] + [T]
+    l, b, ids, off, w, gw = make(T, 72, 5, 0, False, offsets, True, T + S)
+    loss, counts, probs, tokens = forward(l, b, ids, off, 0)
+    want, cnt, mean, n, _ = reference(l, b, ids, off, 0, w, gw)
+    assert torch.equal(counts.cpu().long(), cnt.long()) and torch.equal(tokens.cpu().long(), n.long())
+    # softmax entries: exp of a difference (its rounding, |l - top| <= 16 half ulps, and
+    # the function's few ulps), sums of 72 entries and of T tokens
+    assert ((probs.cpu().double() - mean).abs() <= (16 + 8 + 72 + T + 8) * ref.U32 * mean + 1e-30).all()
+    assert abs(float(loss) - want) <= (16 + 8 + 72 + T + S + 16) * ref.U32 * want
+
+
+def test_one_expert_in_every_slot_is_deterministic():
+    """32 slots with the same id: their gradients add up in the slots' order."""
+    T, E, k = 300, 64, 32
+    gen = torch.Generator().manual_seed(2)
+    l = torch.randn(T, E, generator=gen)
+    ids = torch.full((T, k), 7, dtype=torch.int32)
+    w = torch.rand(T, k, generator=gen)
+    gw = torch.randn(T, k, generator=gen) * 10 ** (4 * torch.rand(T, k, generator=gen))
+    got = [api.moe_route_backward(c(l), None, c(ids), c(w), c(gw), 0)[0] for _ in range(4)]
+    for g in got[1:]:
+        assert torch.equal(g, got[0])
+    d = w.double() * (gw.double() - (gw.double() * w.double()).sum(1, keepdim=True))
+    # the inner sum and the outer one each have 32 terms (5 + 32 roundings of partial sums)
+    inner = (gw.double() * w.double()).abs().sum(1)
+    bound = 40 * ref.U32 * (w.double() * (gw.double().abs() + inner[:, None])).sum(1) * 2
+    assert ((got[0][:, 7].cpu().double() - d.sum(1)).abs() <= bound).all()
+    assert (got[0][:, :7] == 0).all() and (got[0][:, 8:] == 0).all()
