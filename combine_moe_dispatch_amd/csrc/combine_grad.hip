@@ -15,14 +15,15 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr unsigned kMaxBlocks = 1u << 23;  // a launch has less than 2^32 threads
 
 __global__ void __launch_bounds__(kThreads)
 combine_grad_kernel(const uint4* __restrict__ grad_out, const uint4* __restrict__ y,
                     const int32_t* __restrict__ token_row, const float* __restrict__ w,
                     uint4* __restrict__ grad_y, float* __restrict__ grad_w, int nvec, int k,
-                    int rows) {
+                    int rows, unsigned first) {
   __shared__ float s_sum[kThreads / kWave];
-  const size_t pair = blockIdx.x;
+  const size_t pair = first + blockIdx.x;
   const int row = token_row[pair];
   if (row < 0 || row >= rows) {
     if (grad_w && threadIdx.x == 0) grad_w[pair] = 0.0f;
@@ -66,9 +67,14 @@ combine_grad_kernel(const uint4* __restrict__ grad_out, const uint4* __restrict_
 hipError_t launch_combine_grad(const void* grad_out, const void* y, const int32_t* token_row,
                                const float* w, void* grad_y, float* grad_w, int T, int H, int k,
                                int rows, hipStream_t st) {
-  hipLaunchKernelGGL(combine_grad_kernel, dim3((unsigned)T * (unsigned)k), dim3(kThreads), 0, st,
-                     static_cast<const uint4*>(grad_out), static_cast<const uint4*>(y), token_row,
-                     w, static_cast<uint4*>(grad_y), grad_w, H / 8, k, rows);
+  const unsigned pairs = (unsigned)T * (unsigned)k;
+  for (unsigned first = 0; first < pairs; first += kMaxBlocks) {
+    const unsigned left = pairs - first;
+    hipLaunchKernelGGL(combine_grad_kernel, dim3(left < kMaxBlocks ? left : kMaxBlocks),
+                       dim3(kThreads), 0, st, static_cast<const uint4*>(grad_out),
+                       static_cast<const uint4*>(y), token_row, w, static_cast<uint4*>(grad_y),
+                       grad_w, H / 8, k, rows, first);
+  }
   return hipGetLastError();
 }
 

@@ -82,3 +82,27 @@ def test_special_values():
     assert gw[2].isinf().all()
     rows = lay.token_row[[0, 1, 3, 5]].flatten().long()
     assert gy[rows].isfinite().all()
+
+
+def test_more_pairs_than_one_launch_has_blocks():
+    """2^24 pairs and some: every one once."""
+    T, k = (1 << 21) + 3, 8
+    shape = api.Shape(T, 8, 8, k, 1, 0)
+    lay = api.Layout.empty(shape, "cuda")
+    rows = T * k
+    # token t's slot j in row (t, j) of the reversed order; every seventh pair skipped
+    row = torch.arange(rows - 1, -1, -1, dtype=torch.int32, device="cuda").view(T, k)
+    skip = torch.arange(rows, device="cuda").view(T, k) % 7 == 3
+    lay.token_row.copy_(torch.where(skip, -1, row))
+    go = torch.randint(-8, 9, (T, 8), device="cuda").bfloat16()
+    y = torch.randint(-8, 9, (rows, 8), device="cuda").bfloat16()
+    w = torch.randint(1, 5, (T, k), device="cuda").float()
+    gy = torch.full((rows, 8), -77.0, dtype=torch.bfloat16, device="cuda")
+    gw = torch.empty(T, k, device="cuda")
+    api.moe_combine_backward(shape, go, y, lay, w, gy, gw)
+    # small integers: every product and sum is exact
+    pairs = go.float()[:, None, :].expand(T, k, 8)
+    want = torch.where(skip[..., None], -77.0, pairs * w[..., None]).view(rows, 8).flip(0)
+    assert torch.equal(gy.float(), want)
+    dots = (pairs * y.float().flip(0).view(T, k, 8)).sum(2)
+    assert torch.equal(gw, torch.where(skip, 0.0, dots))
