@@ -21,6 +21,7 @@ moe_status from_hip(hipError_t e) {
 moe_status check_shape(const moe_shape* s, int* rows) {
   const int64_t n = moe_recv_rows(s);
   if (n < 0) return moe_combine_partial_recv(s, nullptr, nullptr, nullptr, nullptr);
+  if (n > MOE_MAX_EXPERT_ROWS) return MOE_ERR_UNSUPPORTED;
   *rows = (int)n;
   return MOE_OK;
 }
@@ -61,6 +62,7 @@ moe_status check_router(int32_t T, int32_t E, int32_t k, int32_t score, int32_t 
   if (T < 0 || E < 1 || k < 1 || k > E || S < 1) return MOE_ERR_INVALID_ARG;
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOP_K) return MOE_ERR_UNSUPPORTED;
+  if (T > MOE_MAX_ROUTED || S > MOE_MAX_ROUTED) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)S * E > INT32_MAX || (int64_t)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -954,6 +954,9 @@ bool few_rows(const Segments& s, int u) {
   return rows <= 4 || (rows <= 64 && tiles_of(s, u, Mid::kBu, Mid::kBv) < kUnits);
 }
 
+// A launch has less than 2^32 threads.
+bool launchable(int64_t blocks, int threads) { return blocks < (int64_t(1) << 32) / threads; }
+
 // More than 64 KB of LDS has to be asked for, once per kernel and device.
 template <auto KERNEL, int BYTES>
 hipError_t allow_lds() {
@@ -975,7 +978,7 @@ hipError_t launch_tiles(const MatmulParams& p, hipStream_t st) {
   constexpr int kLds = TileProduct<C, false, false>::kLds;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorNotSupported;
+  if (!launchable(grid, C::kThreads)) return hipErrorNotSupported;
   const hipError_t e = allow_lds<matmul_kernel<C, ACT>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_kernel<C, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p,
@@ -989,7 +992,7 @@ hipError_t launch_stream(const MatmulParams& p, hipStream_t st) {
   constexpr int kCols = Columns<C, ACT>::kTile;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorNotSupported;
+  if (!launchable(grid, Product::kThreads)) return hipErrorNotSupported;
   const hipError_t e = allow_lds<matmul_stream_kernel<Product, ACT>, Product::kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_stream_kernel<Product, ACT>), dim3((unsigned)grid),
@@ -1003,7 +1006,7 @@ hipError_t launch_codes(const MatmulParams& p, hipStream_t st) {
   constexpr int kLds = Fp8Product<C, STAGES>::kLds;
   const int ntiles = (p.F + kCols - 1) / kCols;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorNotSupported;
+  if (!launchable(grid, C::kThreads)) return hipErrorNotSupported;
   const hipError_t e = allow_lds<matmul_fp8_kernel<C, STAGES, ACT>, kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((matmul_fp8_kernel<C, STAGES, ACT>), dim3((unsigned)grid), dim3(C::kThreads), kLds,
@@ -1027,7 +1030,7 @@ hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStrea
   constexpr int kLds = TileProduct<C, true, false>::kLds;
   const int ntiles = (p.K + C::kBu - 1) / C::kBu;
   const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
-  if (grid > INT32_MAX) return hipErrorNotSupported;
+  if (!launchable(grid, C::kThreads)) return hipErrorNotSupported;
   const hipError_t e = allow_lds<grad_x_kernel<C>, kLds>();
   if (e != hipSuccess || grid == 0) return e;
   hipLaunchKernelGGL((grad_x_kernel<C>), dim3((unsigned)grid), dim3(C::kThreads), kLds, st, p, gz,
@@ -1070,6 +1073,7 @@ size_t expert_matmul_grad_workspace(int rows, int pairs, int E, int P, int act) 
 }
 
 hipError_t launch_expert_matmul_grad(const MatmulGradParams& p, hipStream_t st) {
+  if ((int64_t)p.seg.E * p.P > INT32_MAX) return hipErrorNotSupported;  // bias_grad_kernel's threads
   uint16_t* gz = p.act == kActNone ? nullptr : static_cast<uint16_t*>(p.workspace);
   if (p.grad_bias || p.act != kActNone) {
     const int splits = p.seg.pairs == 0 ? 1 : act_splits(p.seg.pairs, p.seg.E, p.F);

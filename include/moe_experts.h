@@ -35,6 +35,10 @@ typedef enum {
 } moe_activation;
 
 #define MOE_MAX_FEATURES (1 << 22)
+/* A tile's rows past the last one still have a 32-bit number. */
+#define MOE_MAX_EXPERT_ROWS (INT32_MAX - 65535)
+/* Tokens, and sequences, of the router's calls. */
+#define MOE_MAX_ROUTED (1 << 30)
 
 /* One linear layer held by every expert (host struct, read during the call).
  * P below is the number of columns before the activation: 2 * out_features for
@@ -71,8 +75,10 @@ typedef struct {
  *   pre           [rows][P] bf16 out, bf16(z), for the backward pass; or NULL.
  * Sums are fp32; with fp8 the products of each 128 columns are summed first
  * and then scaled.  Rows of no segment are neither read for a result nor
- * written.  Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED for E, k, rows
- * or features past the library's limits.
+ * written.  But for the residual, no output may overlap another buffer.
+ * Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED for E, k, features or rows
+ * (MOE_MAX_EXPERT_ROWS) past the library's limits, and for outputs of more tiles
+ * (16 x 64 or larger) than one launch has, 2^23.
  */
 moe_status moe_expert_matmul(const moe_shape *shape, const moe_linear *linear, const void *x,
                              const float *x_scales, const moe_layout *layout,
@@ -159,7 +165,8 @@ size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t num_seqs);
  *   loss          [1] fp32 out.
  *   workspace     moe_balance_loss_workspace_size bytes, 16-byte aligned.
  * Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED past MOE_MAX_EXPERTS,
- * MOE_MAX_TOP_K, 2^31 - 1 entries of an output or pairs.
+ * MOE_MAX_TOP_K, MOE_MAX_ROUTED tokens or sequences, 2^31 - 1 entries of an
+ * output or pairs.
  */
 moe_status moe_balance_loss(const float *logits, const float *bias, const int32_t *topk_ids,
                             int32_t T, int32_t E, int32_t k, int32_t score,

@@ -196,3 +196,19 @@ def test_binding_refuses_cpu_tensors():
     with pytest.raises(api.MoeError):  # the library names what is wrong with the shape
         api.moe_expert_matmul(api.Shape(4, 64, 9, 2, 2, 0), api.Linear(64, 64), t, None, lay, t,
                               None, None, None, t)
+
+
+def test_sizes_past_the_last_32_bit_row():
+    """Rows and tokens whose tiles' numbers would pass 2^31, and grids a launch
+    cannot have: refused before anything is launched."""
+    most = (1 << 31) - 65536
+    for rows in (most + 1, (1 << 31) - 1):
+        shape = (rows, 8, 1, 1, 1, 0, 0)
+        assert matmul(shape=shape) == UNSUPPORTED
+        assert backward(shape=shape) == UNSUPPORTED
+        assert combine(shape=shape) == UNSUPPORTED
+    for call in (balance, route):
+        assert call(T=(1 << 30) + 1, E=1, k=1) == UNSUPPORTED
+    assert balance(E=1, k=1, S=(1 << 30) + 1, off=A) == UNSUPPORTED
+    assert matmul(shape=(65536, 64, 1024, 32, 2, 0, 0), lin=(8, 1 << 22, 0)) == UNSUPPORTED
+    assert backward(shape=(1, 64, 1024, 32, 2, 0, 0), lin=(8, 1 << 22, 0)) == UNSUPPORTED
