@@ -55,6 +55,7 @@ moe_status segments(const moe_shape* s, const moe_layout* lay, int rows, moe::Se
   seg->rows = rows;
   const int64_t pairs = (int64_t)s->num_tokens * s->top_k;
   seg->pairs = (int)(pairs < rows ? pairs : rows);
+  if (seg->pairs == 0) seg->rows = 0;  // no segment, whatever the counts say
   return MOE_OK;
 }
 

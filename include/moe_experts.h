@@ -57,7 +57,10 @@ typedef struct {
  *
  *   z = x[row] * weight[e]^T + bias[e],   y[row] = bf16(act(z) + residual[row])
  *
- *   shape         as given to moe_dispatch; its payload says what x holds.
+ *   shape         as given to moe_dispatch (after moe_dispatch_sources with
+ *                 num_tokens = S*T); its payload says what x holds.  No more
+ *                 than num_tokens * top_k rows may be placed: the launch is
+ *                 sized for these, rows past them may stay unwritten.
  *                 hidden is checked but not used: the columns are the
  *                 linear's, so the same shape serves both projections.
  *   x, x_scales   [rows][K] in the receive layout: bf16, or e4m3 codes with

@@ -366,3 +366,57 @@ def test_many_experts(T, E, k):
     for got, wanted, bound, what in zip((gx.view(torch.bfloat16), gw, gb), want, tol,
                                         ("grad_x", "grad_weight", "grad_bias")):
         ref.check(got, wanted, bound, what)
+
+
+def test_no_tokens_with_counts_of_another_batch():
+    """No pair can be placed, so no row is looked at, whatever stands in the counts."""
+    shape, lin = api.Shape(0, 64, 4, 2, 2, 8), api.Linear(64, 32, 1)
+    lay = api.Layout.empty(shape, "cuda")
+    lay.expert_counts.fill_(3)
+    lay.expert_offsets.copy_(torch.tensor([0, 3, 8, 11]))
+    rows = lambda c: torch.full((16, c), FILL, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    y, gx, w = rows(32), rows(64), weights(4, 32, 64, 0, False)[0]
+    api.moe_expert_matmul(shape, lin, rows(64), None, lay, w, None, None, None, y)
+    gw, gb = torch.full_like(w, FILL), torch.full((4, 32), FILL, device="cuda")
+    api.moe_expert_matmul_backward(shape, lin, rows(32), rows(64), lay, w, rows(32), gx, gw, gb,
+                                   api.alloc_expert_workspace(shape, lin, "cuda"))
+    assert (y == FILL).all() and (gx == FILL).all()
+    assert (gw == 0).all() and (gb == 0).all()
+
+
+@pytest.mark.parametrize("S,T,E,k,N,C", [(3, 40, 8, 2, 4, 64), (5, 7, 6, 3, 2, 0), (2, 128, 4, 1, 1, 256)])
+def test_rows_of_several_sources(S, T, E, k, N, C):
+    """The world's rows after moe_dispatch_sources, and the same through the
+    dense rows of the receive half: the same results."""
+    H, F = 64, 48
+    one = api.Shape(T, H, E, k, N, C)
+    world = api.world_shape(one, S)
+    gen = torch.Generator().manual_seed(S)
+    x = torch.randn(S * T, H, generator=gen).bfloat16().cuda()
+    ids = torch.from_numpy(inputs.random_ids(S * T, k, E, 3, distinct=True)).cuda()
+    lay = api.Layout.empty(world, "cuda")
+    recv, _ = api.alloc_recv(world, "cuda", fill=0xFFFF)
+    counts = torch.empty(S, E, dtype=torch.int32, device="cuda")
+    api.moe_dispatch_sources(one, S, x, ids, recv, None, lay, counts,
+                             torch.empty(E, S, dtype=torch.int32, device="cuda"),
+                             api.alloc_workspace(world, "cuda"))
+    rows = recv.shape[0]
+    w, _ = weights(E, 2 * F, H, 0, False)
+    lin = api.Linear(H, F, ACT["swiglu"])
+    y = torch.full((rows, F), FILL, dtype=torch.bfloat16, device="cuda")
+    api.moe_expert_matmul(world, lin, recv, None, lay, w, None, None, None, y)
+    spans = ref.segments(lay.expert_counts.tolist(), lay.expert_offsets.tolist(), E // N, C)
+    want = ref.matmul(host(recv), host(w), None, None, spans, "swiglu", F)
+    ref.check(y, want[0], want[2], "y", FILL)
+    # packed
+    dense = api.Shape(S * T, H, E, k, N, 0)
+    gx, _ = api.alloc_recv(dense, "cuda", fill=0xFFFF)
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    api.moe_dispatch_recv(world, recv, None, lay, gx, None, off)
+    packed = api.Layout.empty(dense, "cuda")
+    packed.expert_offsets.copy_(off[:E])
+    packed.expert_counts.copy_(off[1:] - off[:E])
+    gy = torch.full((S * T * k, F), FILL, dtype=torch.bfloat16, device="cuda")
+    api.moe_expert_matmul(dense, lin, gx, None, packed, w, None, None, None, gy)
+    for (a, b), o in zip(spans, off.tolist()):
+        assert torch.equal(gy[o:o + b - a], y[a:b])
