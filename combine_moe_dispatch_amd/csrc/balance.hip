@@ -12,8 +12,10 @@
 // loaded before the current one is worked on, rows are 16 bytes a lane where
 // E and the pointers allow, and every wave walks a run of neighbouring tokens,
 // whose sequence is looked up once and whose counts stay in registers.  65536
-// tokens of 256 experts: the gradient 134 MB in 34 us (4.0 TB/s; the columns'
-// sums 4 us more), where a copy would take 26.
+// tokens of 256 experts: the gradient 134 MB in 33 us (4.1 TB/s; the columns'
+// sums 4 us more), where a copy would take 26.  The routed weights come with
+// the row (131072 tokens 81 -> 73 us), the gradients go out past the caches
+// (73 -> 72).
 #include "device_common.h"
 #include "experts.h"
 
@@ -74,17 +76,22 @@ struct Row {
       }
     }
   }
-  template <class T>
-  static __device__ __forceinline__ void store(T* row, int E, const T (&v)[VPL]) {
+  // STREAM: to memory, past the caches
+  template <bool STREAM = false>
+  static __device__ __forceinline__ void store(float* row, int E, const float (&v)[VPL]) {
 #pragma unroll
     for (int i = 0; i < VPL; i += VEC) {
       if (expert(i) >= E) continue;
-      if constexpr (VEC == 4)
-        *reinterpret_cast<int4*>(row + expert(i)) =
-            make_int4(__builtin_bit_cast(int, v[i]), __builtin_bit_cast(int, v[i + 1]),
-                      __builtin_bit_cast(int, v[i + 2]), __builtin_bit_cast(int, v[i + 3]));
-      else
+      if constexpr (VEC == 4) {
+        const uint4 q = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                   __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+        if constexpr (STREAM)
+          store_stream(reinterpret_cast<uint4*>(row + expert(i)), q);
+        else
+          *reinterpret_cast<uint4*>(row + expert(i)) = q;
+      } else {
         row[expert(i)] = v[i];
+      }
     }
   }
 };
@@ -130,21 +137,31 @@ __device__ __forceinline__ void probabilities(const float (&l)[VPL], int score, 
   }
 }
 
-// The tokens of one wave, one after the other: ids and biased logits of the
-// current one, the next one's already on their way.
+// The tokens of one wave, one after the other: ids, biased logits and (if
+// wanted) routed weights and their gradients of the current one, the next one's
+// already on their way.
 template <int VPL, int VEC>
 struct Tokens {
   using R = Row<VPL, VEC>;
   const float* logits;
   const int32_t* ids;
+  const float* weights = nullptr;
+  const float* grad_weights = nullptr;
   int E, k, end, step, t;
   float bias[VPL], l[VPL], ahead[VPL];
   int id, id_ahead;
+  float w, w_ahead, gw, gw_ahead;
 
   __device__ __forceinline__ void fetch(int at) {
     if (at >= end) return;
     R::load(logits + (size_t)at * E, E, ahead, -INFINITY);
-    id_ahead = lane_id() < k ? ids[(size_t)at * k + lane_id()] : -1;
+    const bool slot = lane_id() < k;
+    const size_t pair = (size_t)at * k + lane_id();
+    id_ahead = slot ? ids[pair] : -1;
+    if (grad_weights) {
+      w_ahead = slot ? weights[pair] : 0.0f;
+      gw_ahead = slot ? grad_weights[pair] : 0.0f;
+    }
   }
   __device__ __forceinline__ void init(const float* lg, const float* bs, const int32_t* id_list,
                                        int E_, int k_, int first, int end_, int step_) {
@@ -170,6 +187,8 @@ struct Tokens {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) l[i] = ahead[i] + bias[i];
     id = id_ahead;
+    w = w_ahead;
+    gw = gw_ahead;
     fetch(t + step);
     return true;
   }
@@ -447,6 +466,8 @@ route_grad_kernel(RouteGradParams q, int per_wave) {
   R::store(s_row[wave], VPL * kWave, g);
   int seq = 0, seq_from = 0, seq_to = -1;  // none yet
   Tokens<VPL, VEC> tok;
+  tok.weights = q.weights;
+  tok.grad_weights = q.grad_weights;
   tok.init(q.logits, q.bias, q.ids, q.E, q.k, t0, t1, 1);
   while (tok.next()) {
     float* out = q.grad_logits + (size_t)tok.t * q.E;
@@ -455,7 +476,7 @@ route_grad_kernel(RouteGradParams q, int per_wave) {
     if (__ballot(real) == 0) {  // a padded token, whatever its logits hold
 #pragma unroll
       for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
-      R::store(out, q.E, d);
+      R::template store<true>(out, q.E, d);
       continue;
     }
     if (q.counts && tok.t >= seq_to) {  // the first token, or past the sequence
@@ -483,11 +504,7 @@ route_grad_kernel(RouteGradParams q, int per_wave) {
       total += e[i];
       weighted = fmaf(g[i], e[i], weighted);
     }
-    float w = 0.0f, gw = 0.0f;
-    if (q.grad_weights && real) {
-      w = q.weights[(size_t)tok.t * q.k + lane];
-      gw = q.grad_weights[(size_t)tok.t * q.k + lane];
-    }
+    const float w = real ? tok.w : 0.0f, gw = real ? tok.gw : 0.0f;
     total = wave_sum(total);
     weighted = wave_sum(weighted);
     const float inv = inside ? 1.0f / total : 0.0f;
@@ -511,7 +528,7 @@ route_grad_kernel(RouteGradParams q, int per_wave) {
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) d[i] *= r[i];
-    R::store(out, q.E, d);
+    R::template store<true>(out, q.E, d);
     if constexpr (BIAS) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) sum[i] += d[i];
