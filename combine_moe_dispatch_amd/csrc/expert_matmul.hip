@@ -841,7 +841,9 @@ grad_x_kernel(MatmulGradParams p, const uint16_t* gz, int ntiles) {
 // expert a tile is a handful of steps and a large result, so the blocks stay:
 // each takes one tile after another and starts the loads of the next before
 // it stores the last, without waiting for those stores.  32 experts of 256 rows,
-// 4096 x 7168: 1.9 GB written in 810 us; without the stores it takes 575 us.
+// 4096 x 7168: 1.9 GB written in 800 us (810 before half steps were left out,
+// 575 of them without the stores); a tile's steps take 9.7 us, the next one's
+// loads 1.8, the stores 4.4.
 // Streaming stores took 1130 us, device-scope ones 1080, 128 x 128 tiles with
 // two blocks to a compute unit 1030.
 template <class C>
