@@ -7,7 +7,8 @@
  * stream, no allocation, no synchronisation, no state between calls; errors
  * the host can see are returned and launch nothing.  Every call can be
  * captured in a HIP graph; a workspace belongs to one call at a time, so
- * graphs that may run at once need workspaces of their own.
+ * graphs that may run at once need workspaces of their own.  Unless a call
+ * says otherwise its outputs overlap none of its other buffers.
  *
  * The gradient of moe_dispatch itself (each token's gradient is the sum of its
  * pairs' rows) is moe_combine with all weights one.
@@ -78,7 +79,7 @@ typedef struct {
  *   pre           [rows][P] bf16 out, bf16(z), for the backward pass; or NULL.
  * Sums are fp32; with fp8 the products of each 128 columns are summed first
  * and then scaled.  Rows of no segment are neither read for a result nor
- * written.  But for the residual, no output may overlap another buffer.
+ * written.
  * Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED for E, k, features or rows
  * (MOE_MAX_EXPERT_ROWS) past the library's limits, and for outputs of more tiles
  * (16 x 64 or larger) than one launch has, 2^23.
@@ -132,7 +133,6 @@ moe_status moe_expert_matmul_backward(const moe_shape *shape, const moe_linear *
  *   A pair with token_row -1 has grad_weights 0 and no row; rows no pair
  *   reaches are not written.  Either output may be NULL (not wanted, not both);
  *   expert_y is read for grad_weights only, topk_weights for grad_y only.
- *   grad_y may not overlap expert_y.
  */
 moe_status moe_combine_backward(const moe_shape *shape, const void *grad_out,
                                 const void *expert_y, const moe_layout *layout,
