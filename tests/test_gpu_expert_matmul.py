@@ -420,3 +420,9 @@ def test_rows_of_several_sources(S, T, E, k, N, C):
     api.moe_expert_matmul(dense, lin, gx, None, packed, w, None, None, None, gy)
     for (a, b), o in zip(spans, off.tolist()):
         assert torch.equal(gy[o:o + b - a], y[a:b])
+
+
+@pytest.mark.parametrize("counts,F", [([2300, 120, 2050], 2816 + 8), ([4100], 4096)])
+def test_groups_of_row_tiles(counts, F):
+    """More row tiles of an expert than run through together, in equal and in unequal groups."""
+    run(sum(counts), len(counts), 1, 1, 0, 64, F, "none", residual=False, pre=False, counts=counts)
