@@ -133,6 +133,22 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _empty(stream, size, dtype, device, returned: bool = True) -> torch.Tensor:
+    """Memory that a call on `stream` allocates for itself: from that stream's
+    pool, whose blocks no other stream's queued work still uses.  If the caller
+    gets it, the current stream is recorded, so that a dropped tensor is not
+    reused while work queued there reads it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(size, dtype=dtype, device=device)
+    own = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(own):
+        t = torch.empty(size, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 # ---------------------------------------------------------------------------
 # Argument checks made before each C call: every tensor must be a contiguous
 # GPU tensor of the expected element type holding at least the elements the
@@ -466,7 +482,8 @@ def alloc_workspace(shape: Shape, device) -> Optional[torch.Tensor]:
 # ---------------------------------------------------------------------------
 # include/moe_experts.h: the experts' matrix product, the balance loss and the
 # gradients.  These calls run on the device of their tensors, which must all be
-# on one; without a stream they use that device's current one.
+# on one; without a stream they use that device's current one.  What a call
+# allocates (results not given, a workspace) comes from its stream's pool.
 # ---------------------------------------------------------------------------
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = 0, 1, 2, 3
 
@@ -565,19 +582,13 @@ def _run(call: str, dev: int, stream, fn, *args) -> None:
             _check(fn(*args, handle), call)
 
 
-def _workspace(nbytes: int, given, dev: int, stream, call: str):
-    """The caller's workspace, or one of the call's own (kept from reuse until
-    the stream has passed it)."""
+def _workspace(nbytes: int, given, dev: int, stream):
+    """The caller's workspace, or one of the call's own."""
     if given is not None or nbytes == 0:
         return given
     if dev < 0:
         return None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(_stream(stream), device=torch.device("cuda", dev))
-        ws.record_stream(s)
-    return ws
+    return _empty(stream, nbytes, torch.uint8, torch.device("cuda", dev), returned=False)
 
 
 def _nbytes(t: Optional[torch.Tensor]) -> int:
@@ -703,13 +714,13 @@ def moe_balance_loss(logits: torch.Tensor, bias: Optional[torch.Tensor], topk_id
     S = _num_seqs(c, seq_offsets)
     dev = logits.device
     if expert_counts is None:
-        expert_counts = torch.empty(S, E, dtype=torch.int32, device=dev)
+        expert_counts = _empty(stream, (S, E), torch.int32, dev)
     if expert_probs is None:
-        expert_probs = torch.empty(S, E, dtype=torch.float32, device=dev)
+        expert_probs = _empty(stream, (S, E), torch.float32, dev)
     if seq_tokens is None:
-        seq_tokens = torch.empty(S, dtype=torch.int32, device=dev)
+        seq_tokens = _empty(stream, S, torch.int32, dev)
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        loss = _empty(stream, 1, torch.float32, dev)
     d = _all(c, (("logits", logits, _F32, T * E, True), ("bias", bias, _F32, E, False),
                  ("topk_ids", topk_ids, _I32, T * k, True),
                  ("seq_offsets", seq_offsets, _I32, S + 1, False),
@@ -717,7 +728,7 @@ def moe_balance_loss(logits: torch.Tensor, bias: Optional[torch.Tensor], topk_id
                  ("expert_probs", expert_probs, _F32, S * E, True),
                  ("seq_tokens", seq_tokens, _I32, S, True), ("loss", loss, _F32, 1, True),
                  ("workspace", workspace, _BYTES, 0, False)))
-    ws = _workspace(_lib.moe_balance_loss_workspace_size(T, E, S), workspace, d, stream, c)
+    ws = _workspace(_lib.moe_balance_loss_workspace_size(T, E, S), workspace, d, stream)
     _run(c, d, stream, _lib.moe_balance_loss, _ptr(logits), _ptr(bias), _ptr(topk_ids), T, E, k,
          score, _ptr(seq_offsets), S, coef, _ptr(expert_counts), _ptr(expert_probs),
          _ptr(seq_tokens), _ptr(loss), _ptr(ws), _nbytes(ws))
@@ -745,9 +756,9 @@ def moe_route_backward(logits: torch.Tensor, bias: Optional[torch.Tensor], topk_
     S = _num_seqs(c, seq_offsets)
     dev = logits.device
     if grad_logits is None:
-        grad_logits = torch.empty(T, E, dtype=torch.float32, device=dev)
+        grad_logits = _empty(stream, (T, E), torch.float32, dev)
     if grad_bias is None and with_grad_bias:
-        grad_bias = torch.empty(E, dtype=torch.float32, device=dev)
+        grad_bias = _empty(stream, E, torch.float32, dev)
     d = _all(c, (("logits", logits, _F32, T * E, True), ("bias", bias, _F32, E, False),
                  ("topk_ids", topk_ids, _I32, T * k, True),
                  ("topk_weights", topk_weights, _F32, T * k, grad_weights is not None),
@@ -760,7 +771,7 @@ def moe_route_backward(logits: torch.Tensor, bias: Optional[torch.Tensor], topk_
                  ("grad_bias", grad_bias, _F32, E, False),
                  ("workspace", workspace, _BYTES, 0, False)))
     need = 0 if grad_bias is None else _lib.moe_route_backward_workspace_size(T, E)
-    ws = _workspace(need, workspace, d, stream, c)
+    ws = _workspace(need, workspace, d, stream)
     _run(c, d, stream, _lib.moe_route_backward, _ptr(logits), _ptr(bias), _ptr(topk_ids),
          _ptr(topk_weights), _ptr(grad_weights), T, E, k, score, _ptr(seq_offsets), S, coef,
          _ptr(expert_counts), _ptr(seq_tokens), _ptr(grad_loss), _ptr(grad_logits),
