@@ -232,9 +232,9 @@ def moe_route_topk(logits: torch.Tensor, bias: Optional[torch.Tensor], k: int, s
     """Top-k routing; returns (topk_ids int32 [T,k], topk_weights fp32 [T,k])."""
     T, E = logits.shape
     if topk_ids is None:
-        topk_ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        topk_ids = _empty(stream, (T, k), torch.int32, logits.device)
     if topk_weights is None:
-        topk_weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+        topk_weights = _empty(stream, (T, k), torch.float32, logits.device)
     _route_args("moe_route_topk", logits, bias, k, topk_ids, topk_weights)
     _check(_lib.moe_route_topk(_ptr(logits), _ptr(bias), T, E, k, score, _ptr(topk_ids),
                                _ptr(topk_weights), _stream(stream)), "moe_route_topk")
@@ -248,9 +248,9 @@ def moe_route_topk_grouped(logits: torch.Tensor, bias: Optional[torch.Tensor], k
     """Group-limited top-k routing; returns (topk_ids, topk_weights)."""
     T, E = logits.shape
     if topk_ids is None:
-        topk_ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        topk_ids = _empty(stream, (T, k), torch.int32, logits.device)
     if topk_weights is None:
-        topk_weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+        topk_weights = _empty(stream, (T, k), torch.float32, logits.device)
     _route_args("moe_route_topk_grouped", logits, bias, k, topk_ids, topk_weights)
     _check(_lib.moe_route_topk_grouped(_ptr(logits), _ptr(bias), T, E, k, score, n_groups,
                                        topk_groups, _ptr(topk_ids), _ptr(topk_weights),

@@ -30,6 +30,17 @@ def route_backward(r, stream=None):
                                   with_grad_bias=True, stream=stream)
 
 
+def route(r, stream=None):
+    return api.moe_route_topk(r["logits"], None, K, 1, stream=stream)
+
+
+def route_grouped(r, stream=None):
+    return api.moe_route_topk_grouped(r["logits"], None, K, 1, 8, 4, stream=stream)
+
+
+CALLS = [balance, route_backward, route, route_grouped]
+
+
 def pending(sizes):
     """Queue a few milliseconds of products on the current stream, then writes to
     blocks of these sizes, and free them while all of it is pending."""
@@ -43,14 +54,16 @@ def pending(sizes):
         b.fill_(0x5A)
 
 
-@pytest.mark.parametrize("call", [balance, route_backward])
+@pytest.mark.parametrize("call", CALLS)
 @pytest.mark.parametrize("as_handle", [False, True])
 def test_blocks_freed_with_work_pending(routed, call, as_handle):
     want = call(routed)
     want_host = [t.cpu() for t in want]
     sizes = [t.numel() * t.element_size() for t in want]
-    sizes.append(api.moe_balance_loss_workspace_size(T, E, 1) if call is balance
-                 else api.moe_route_backward_workspace_size(T, E))
+    if call is balance:
+        sizes.append(api.moe_balance_loss_workspace_size(T, E, 1))
+    elif call is route_backward:
+        sizes.append(api.moe_route_backward_workspace_size(T, E))
     st = torch.cuda.Stream()
     for _ in range(2):
         pending(sizes)
@@ -60,7 +73,7 @@ def test_blocks_freed_with_work_pending(routed, call, as_handle):
             assert torch.equal(g.cpu(), w)
 
 
-@pytest.mark.parametrize("call", [balance, route_backward])
+@pytest.mark.parametrize("call", CALLS)
 def test_dropped_results_are_not_reused_while_they_are_read(routed, call):
     want = [t.cpu() for t in call(routed)]
     st = torch.cuda.Stream()

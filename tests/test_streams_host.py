@@ -85,7 +85,16 @@ def route_backward(stream):
                                   with_grad_bias=True, stream=stream)
 
 
-@pytest.mark.parametrize("call,results,own", [(balance, 4, 5), (route_backward, 2, 3)])
+def route(stream):
+    return api.moe_route_topk(cuda(torch.zeros(T, E)), None, K, 0, stream=stream)
+
+
+def route_grouped(stream):
+    return api.moe_route_topk_grouped(cuda(torch.zeros(T, E)), None, K, 0, 8, 4, stream=stream)
+
+
+@pytest.mark.parametrize("call,results,own", [(balance, 4, 5), (route_backward, 2, 3),
+                                              (route, 2, 2), (route_grouped, 2, 2)])
 @pytest.mark.parametrize("given", [lambda: Stream(9), lambda: 9])
 def test_on_a_given_stream(seen, call, results, own, given):
     out = call(given())
@@ -94,11 +103,12 @@ def test_on_a_given_stream(seen, call, results, own, given):
     # every result, and it alone, is recorded on the stream of the caller
     assert all(s == 7 for _, s in seen.recorded)
     assert {id(t) for t, _ in seen.recorded} == {id(t) for t in out}
-    # the workspace that the library was given is the one made there
+    # the library was given what was made there, the workspace among it
     assert {t.data_ptr() for t, _ in seen.made} <= set(seen.pointers[0])
 
 
-@pytest.mark.parametrize("call,own", [(balance, 5), (route_backward, 3)])
+@pytest.mark.parametrize("call,own", [(balance, 5), (route_backward, 3), (route, 2),
+                                      (route_grouped, 2)])
 def test_on_the_current_stream(seen, call, own):
     call(None)
     assert seen.launched == [7] and [s for _, s in seen.made] == [7] * own
