@@ -574,6 +574,8 @@ def _run(call: str, dev: int, stream, fn, *args) -> None:
     if dev < 0:  # nothing to launch on: the library names what is wrong
         _check(fn(*args, None), call)
         return
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"{call}: stream is on cuda:{stream.device_index}, tensors on cuda:{dev}")
     handle = _raw_stream(dev) if stream is None else _stream(stream)
     if dev == torch.cuda.current_device():
         _check(fn(*args, handle), call)

@@ -113,3 +113,15 @@ def test_on_the_current_stream(seen, call, own):
     call(None)
     assert seen.launched == [7] and [s for _, s in seen.made] == [7] * own
     assert seen.recorded == []
+
+
+@pytest.mark.parametrize("call", [balance, route_backward])
+def test_a_stream_of_another_device_is_refused(seen, call):
+    other = Stream(9)
+    other.device_index = 1
+    with pytest.raises(ValueError, match="stream is on cuda:1, tensors on cuda:0"):
+        call(other)
+    assert seen.launched == []
+    other.device_index = 0
+    call(other)
+    assert seen.launched == [9]
