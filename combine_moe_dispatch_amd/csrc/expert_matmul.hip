@@ -1077,7 +1077,7 @@ size_t expert_matmul_grad_workspace(int rows, int pairs, int E, int P, int act) 
 }
 
 hipError_t launch_expert_matmul_grad(const MatmulGradParams& p, hipStream_t st) {
-  if ((int64_t)p.seg.E * p.P > INT32_MAX) return hipErrorNotSupported;  // bias_grad_kernel's threads
+  if (p.grad_bias && (int64_t)p.seg.E * p.P > INT32_MAX) return hipErrorNotSupported;
   uint16_t* gz = p.act == kActNone ? nullptr : static_cast<uint16_t*>(p.workspace);
   if (p.grad_bias || p.act != kActNone) {
     const int splits = p.seg.pairs == 0 ? 1 : act_splits(p.seg.pairs, p.seg.E, p.F);

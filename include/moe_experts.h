@@ -82,7 +82,7 @@ typedef struct {
  * written.
  * Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED for E, k, features or rows
  * (MOE_MAX_EXPERT_ROWS) past the library's limits, and for outputs of more tiles
- * (16 x 64 or larger) than one launch has, 2^23.
+ * (16 x 64 or larger) than one launch has: 2^24, fp8 2^23.
  */
 moe_status moe_expert_matmul(const moe_shape *shape, const moe_linear *linear, const void *x,
                              const float *x_scales, const moe_layout *layout,
@@ -115,6 +115,8 @@ size_t moe_expert_matmul_backward_workspace_size(const moe_shape *shape,
  *                 rounded to bf16, which the two products read (grad_bias is
  *                 summed before that rounding), and parts of those sums.  NULL
  *                 is allowed for MOE_ACT_NONE without grad_bias.
+ * Errors as moe_expert_matmul; MOE_ERR_UNSUPPORTED also for a grad_bias of more
+ * than 2^31 - 1 entries and a grad_weight of more than 2^31 - 1 tiles.
  */
 moe_status moe_expert_matmul_backward(const moe_shape *shape, const moe_linear *linear,
                                       const void *grad_y, const void *x,
