@@ -101,14 +101,14 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const void* base, uint
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds), "v"(offset), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 // 4 bytes a lane from an address of its own, lane i at lds + 4 i.
 __device__ __forceinline__ void load4_to_lds(uint32_t lds, const void* p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :
                : "s"(lds), "v"(p)
-               : "memory");
+               : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -130,7 +130,7 @@ __device__ __forceinline__ void mfma_in_place(f32x4_t& c, bf16x8_t a, bf16x8_t b
 // masked: those pass through here.  (The two states in front of every product
 // take 1% of a prefill's time.)
 __device__ __forceinline__ void operand_written(bf16x8_t& v) { asm volatile("s_nop 1" : "+v"(v)); }
-// The last product's results get written (8 passes of 4 cycles).
+// The last product's results get written (8 wait states would do).
 __device__ __forceinline__ void mfma_results() { asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15"); }
 __device__ __forceinline__ void mfma_result(f32x4_t& c) { asm volatile("" : "+a"(c)); }
 
