@@ -854,7 +854,7 @@ grad_x_kernel(MatmulGradParams p, const uint16_t* gz, int ntiles) {
 // 575 of them without the stores); a tile's steps take 9.7 us, the next one's
 // loads 1.8, the stores 4.4.
 // Streaming stores took 1130 us, device-scope ones 1080, 128 x 128 tiles with
-// two blocks to a compute unit 1030.
+// two blocks to a compute unit 936.
 template <class C>
 __global__ void __launch_bounds__(C::kThreads)
 grad_w_kernel(MatmulGradParams p, const uint16_t* gz, unsigned nt, unsigned pt) {
@@ -967,6 +967,18 @@ bool few_rows(const Segments& s, int u) {
   return rows <= 4 || (rows <= 64 && tiles_of(s, u, Mid::kBu, Mid::kBv) < kUnits);
 }
 
+// The weight gradient has every expert's tiles whatever the counts: large
+// ones above 64 rows an expert, if they give three quarters of the compute units
+// one (one expert of 2048 x 4096, 4096 rows, 128 large tiles: 100 us against 68;
+// 2048 x 6144, 1024 rows, 192 tiles: 36.7 against 37.3; 4096 x 4096, 8192 rows,
+// 256 tiles: 202 against 259; 32 experts of 4096 x 7168, 256 rows: 808 against
+// 936; 256 of 512 x 512, 32 rows: 35 against 30).
+bool large_weight_tiles(const Segments& s, int K, int P) {
+  const int64_t tiles = (int64_t)s.E * ((K + Large::kBu - 1) / Large::kBu) *
+                        ((P + Large::kBv - 1) / Large::kBv);
+  return s.pairs / s.E > 64 && tiles >= kUnits * 3 / 4;
+}
+
 // A launch has less than 2^32 threads.
 bool launchable(int64_t blocks, int threads) { return blocks < (int64_t(1) << 32) / threads; }
 
@@ -1051,7 +1063,8 @@ hipError_t launch_grad_x(const MatmulGradParams& p, const uint16_t* gz, hipStrea
   return hipGetLastError();
 }
 
-template <class C>
+// BLOCKS to a compute unit.
+template <class C, int BLOCKS>
 hipError_t launch_grad_w(const MatmulGradParams& p, const uint16_t* gz, hipStream_t st) {
   constexpr int kLds = TileProduct<C, true, true>::kLds + kTableBytes;
   const unsigned nt = (p.K + C::kBu - 1) / C::kBu, pt = (p.P + C::kBv - 1) / C::kBv;
@@ -1059,7 +1072,8 @@ hipError_t launch_grad_w(const MatmulGradParams& p, const uint16_t* gz, hipStrea
   if (tiles > INT32_MAX) return hipErrorNotSupported;
   const hipError_t e = allow_lds<grad_w_kernel<C>, kLds>();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((grad_w_kernel<C>), dim3((unsigned)(tiles < kUnits ? tiles : kUnits)),
+  constexpr int kMost = kUnits * BLOCKS;
+  hipLaunchKernelGGL((grad_w_kernel<C>), dim3((unsigned)(tiles < kMost ? tiles : kMost)),
                      dim3(C::kThreads), kLds, st, p, gz, nt, pt);
   return hipGetLastError();
 }
@@ -1117,8 +1131,8 @@ hipError_t launch_expert_matmul_grad(const MatmulGradParams& p, hipStream_t st) 
   if (e == hipSuccess && p.grad_x)
     e = large ? launch_grad_x<Large>(p, g, st) : launch_grad_x<Mid>(p, g, st);
   if (e == hipSuccess && p.grad_weight)
-    e = (int64_t)p.K * p.P >= 256 * 256 ? launch_grad_w<Large>(p, g, st)
-                                        : launch_grad_w<Mid>(p, g, st);
+    e = large_weight_tiles(p.seg, p.K, p.P) ? launch_grad_w<Large, 1>(p, g, st)
+                                            : launch_grad_w<Mid, 2>(p, g, st);
   return e;
 }
 
