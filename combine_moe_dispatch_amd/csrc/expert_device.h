@@ -12,8 +12,6 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActSwiglu = 3 };
 
-__device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
 // Rows [begin, end) of expert e that hold placed pairs: its counts cut at its
 // rank's capacity, and at the buffer whatever the metadata says.
 __device__ __forceinline__ void segment_of(const Segments& s, int e, int& begin, int& end) {
