@@ -2,6 +2,7 @@
 // caller's stream.  No allocation, no synchronisation, no state.
 #include "moe_experts.h"
 #include "experts.h"
+#include "shape_check.h"
 
 namespace {
 
@@ -15,12 +16,12 @@ moe_status from_hip(hipError_t e) {
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
-// A shape's receive rows.  For a bad shape the combine's second half, which
-// checks the shape before anything else and finds nothing to launch, names
-// the error.
+// A shape's receive rows.
 moe_status check_shape(const moe_shape* s, int* rows) {
-  const int64_t n = moe_recv_rows(s);
-  if (n < 0) return moe_combine_partial_recv(s, nullptr, nullptr, nullptr, nullptr);
+  int L;
+  int64_t n;
+  const moe_status st = moe::check_shape(s, &L, &n);
+  if (st != MOE_OK) return st;
   if (n > MOE_MAX_EXPERT_ROWS) return MOE_ERR_UNSUPPORTED;
   *rows = (int)n;
   return MOE_OK;
