@@ -958,13 +958,17 @@ bool large_codes(const Segments& s, int u) {
   return s.pairs / s.E > Codes::kBv / 4 && tiles_of(s, u, Codes::kBu, Codes::kBv) >= kUnits;
 }
 
-// The streaming product for up to 4 rows an expert (one token of 8 of 32
-// experts, 4096 x 7168: 82 us against 110 on 128 x 128 tiles; 16 tokens 301
-// against 299), and while those tiles would leave compute units idle, up to
-// 64 (one expert, 64 rows, 2048 x 7168: 21 us against 63).
+// The streaming product for up to 4 rows an expert and 128 in all (one token of
+// 8 of 32 experts, 4096 x 7168: 82 us against 110 on 128 x 128 tiles; 128 rows
+// of 32 experts, 4 each 316 against 317, in 8 of them 88 against 114; 256 rows of
+// 256 experts, one each 2.49 ms for either, in 8 of them 179 us against 106, in
+// one 137 against 71: its 16 row tiles read the weights again), and while those
+// tiles would leave compute units idle, up to 64 an expert (one expert, 64 rows,
+// 2048 x 7168: 21 us against 63).
 bool few_rows(const Segments& s, int u) {
   const int64_t rows = s.pairs / s.E;
-  return rows <= 4 || (rows <= 64 && tiles_of(s, u, Mid::kBu, Mid::kBv) < kUnits);
+  return (rows <= 4 && s.pairs <= 128) ||
+         (rows <= 64 && tiles_of(s, u, Mid::kBu, Mid::kBv) < kUnits);
 }
 
 // The weight gradient has every expert's tiles whatever the counts: large
