@@ -12,7 +12,7 @@
 // loaded before the current one is worked on, rows are 16 bytes a lane where
 // E and the pointers allow, and every wave walks a run of neighbouring tokens,
 // whose sequence is looked up once and whose counts stay in registers.  65536
-// tokens of 256 experts: the gradient 134 MB in 32 us (4.2 TB/s; the columns'
+// tokens of 256 experts: the gradient 134 MB in 32 to 34 us (4 TB/s; the columns'
 // sums 4 us more), where a copy would take 26.  The routed weights come with
 // the row (131072 tokens 81 -> 73 us), the gradients go out past the caches
 // (73 -> 72).
