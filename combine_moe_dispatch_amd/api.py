@@ -798,3 +798,207 @@ def _num_seqs(call, seq_offsets) -> int:
     if seq_offsets.numel() < 2:
         raise ValueError(f"{call}: seq_offsets must hold one sequence at least")
     return seq_offsets.numel() - 1
+
+
+# ---------------------------------------------------------------------------
+# include/moe_ffn.h: an expert layer in 8 bits (the norm in front, weights to 8
+# bits, the gated feed-forward block and the gradients), as the calls above.
+# ---------------------------------------------------------------------------
+MOE_TYPE_BF16, MOE_TYPE_FP32 = 0, 1
+
+
+class _Ffn(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("intermediate", ctypes.c_int32)]
+
+
+_ffn_p = ctypes.POINTER(_Ffn)
+_lib.moe_rms_norm.argtypes = [_vp, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.moe_rms_norm.restype = _i32
+_lib.moe_rms_norm_backward_workspace_size.argtypes = [_i32, _i32]
+_lib.moe_rms_norm_backward_workspace_size.restype = _size
+_lib.moe_rms_norm_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _size,
+                                       _vp]
+_lib.moe_rms_norm_backward.restype = _i32
+_lib.moe_quantize_weight.argtypes = [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp]
+_lib.moe_quantize_weight.restype = _i32
+_lib.moe_expert_ffn_workspace_size.argtypes = [_shape_p, _ffn_p]
+_lib.moe_expert_ffn_workspace_size.restype = _size
+_lib.moe_expert_ffn.argtypes = [_shape_p, _ffn_p, _vp, _vp, _layout_p, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _size, _vp]
+_lib.moe_expert_ffn.restype = _i32
+_lib.moe_expert_ffn_backward_workspace_size.argtypes = [_shape_p, _ffn_p]
+_lib.moe_expert_ffn_backward_workspace_size.restype = _size
+_lib.moe_expert_ffn_backward.argtypes = [_shape_p, _ffn_p, _vp, _vp, _vp, _layout_p, _vp, _vp, _vp,
+                                         _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]
+_lib.moe_expert_ffn_backward.restype = _i32
+
+
+@dataclasses.dataclass(frozen=True)
+class Ffn:
+    """The gated feed-forward block of every expert (mirrors moe_ffn)."""
+    hidden: int
+    intermediate: int
+
+    def c(self) -> _Ffn:
+        return _Ffn(self.hidden, self.intermediate)
+
+
+def _matrix(call: str, name: str, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{call}: {name} must be a 2-D tensor [T, H]")
+    return t.shape
+
+
+def moe_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor,
+                 eps: float, total: Optional[torch.Tensor], y: Optional[torch.Tensor],
+                 codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                 inv_rms: Optional[torch.Tensor] = None, stream=None) -> None:
+    """total = x + residual; y (bf16) and codes with scales (e4m3) = total / rms * weight.
+    Outputs that are None are not made."""
+    c = "moe_rms_norm"
+    T, H = _matrix(c, "x", x)
+    dev = _all(c, (("x", x, _BF16, T * H, True), ("residual", residual, _BF16, T * H, False),
+                   ("weight", weight, _F32, H, True), ("total", total, _BF16, T * H, False),
+                   ("y", y, _BF16, T * H, False), ("codes", codes, _E4M3, T * H, False),
+                   ("scales", scales, _F32, T * (H // 128), False),
+                   ("inv_rms", inv_rms, _F32, T, False)))
+    _run(c, dev, stream, _lib.moe_rms_norm, _ptr(x), _ptr(residual), _ptr(weight), T, H, eps,
+         _ptr(total), _ptr(y), _ptr(codes), _ptr(scales), _ptr(inv_rms))
+
+
+def moe_rms_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(_lib.moe_rms_norm_backward_workspace_size(T, H))
+
+
+def alloc_rms_norm_workspace(T: int, H: int, device) -> Optional[torch.Tensor]:
+    """Workspace of moe_rms_norm_backward (None when none is needed)."""
+    n = moe_rms_norm_backward_workspace_size(T, H)
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_rms_norm_backward(grad_y: torch.Tensor, total: torch.Tensor, weight: torch.Tensor,
+                          inv_rms: torch.Tensor, carried: Optional[torch.Tensor],
+                          grad_x: Optional[torch.Tensor], grad_weight: Optional[torch.Tensor],
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_rms_norm; either output may be None."""
+    c = "moe_rms_norm_backward"
+    T, H = _matrix(c, "grad_y", grad_y)
+    dev = _all(c, (("grad_y", grad_y, _BF16, T * H, True), ("total", total, _BF16, T * H, True),
+                   ("weight", weight, _F32, H, True), ("inv_rms", inv_rms, _F32, T, True),
+                   ("carried", carried, _BF16, T * H, False),
+                   ("grad_x", grad_x, _BF16, T * H, False),
+                   ("grad_weight", grad_weight, _F32, H, False),
+                   ("workspace", workspace, _BYTES, 0, False)))
+    need = 0 if grad_weight is None else _lib.moe_rms_norm_backward_workspace_size(T, H)
+    ws = _workspace(need, workspace, dev, stream)
+    _run(c, dev, stream, _lib.moe_rms_norm_backward, _ptr(grad_y), _ptr(total), _ptr(weight),
+         _ptr(inv_rms), _ptr(carried), T, H, _ptr(grad_x), _ptr(grad_weight), _ptr(ws),
+         _nbytes(ws))
+
+
+def moe_quantize_weight(weight: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                        stream=None) -> None:
+    """bf16 or fp32 weights [E, P, K] (or [P, K]) to e4m3 in 128 x 128 blocks."""
+    c = "moe_quantize_weight"
+    if not isinstance(weight, torch.Tensor) or weight.dim() not in (2, 3):
+        raise ValueError(f"{c}: weight must be a tensor [E, P, K] or [P, K]")
+    E, P, K = (1, *weight.shape)[-3:]
+    n = E * P * K
+    dev = _all(c, (("weight", weight, (torch.bfloat16, torch.float32), n, True),
+                   ("codes", codes, _E4M3, n, True),
+                   ("scales", scales, _F32, E * (P // 128) * (K // 128), True)))
+    kind = MOE_TYPE_FP32 if weight.dtype == torch.float32 else MOE_TYPE_BF16
+    _run(c, dev, stream, _lib.moe_quantize_weight, _ptr(weight), kind, E, P, K, _ptr(codes),
+         _ptr(scales))
+
+
+def moe_expert_ffn_workspace_size(shape: Shape, ffn: Ffn) -> int:
+    return int(_lib.moe_expert_ffn_workspace_size(ctypes.byref(shape.c()), ctypes.byref(ffn.c())))
+
+
+def moe_expert_ffn_backward_workspace_size(shape: Shape, ffn: Ffn) -> int:
+    return int(_lib.moe_expert_ffn_backward_workspace_size(ctypes.byref(shape.c()),
+                                                           ctypes.byref(ffn.c())))
+
+
+def alloc_ffn_workspace(shape: Shape, ffn: Ffn, device,
+                        backward: bool = False) -> Optional[torch.Tensor]:
+    """Workspace of moe_expert_ffn or moe_expert_ffn_backward (None when none is needed)."""
+    size = moe_expert_ffn_backward_workspace_size if backward else moe_expert_ffn_workspace_size
+    n = size(shape, ffn)
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _ffn_weights(shape: Shape, ffn: Ffn, up, up_scales, down, down_scales, need_up: bool,
+                 need_down: bool):
+    E, H, I = shape.num_experts, ffn.hidden, ffn.intermediate
+    blocks = E * (I // 128) * (H // 128)
+    return (("up", up, _E4M3, 2 * E * I * H, need_up),
+            ("up_scales", up_scales, _F32, 2 * blocks, need_up),
+            ("down", down, _E4M3, E * I * H, need_down),
+            ("down_scales", down_scales, _F32, blocks, need_down))
+
+
+def moe_expert_ffn(shape: Shape, ffn: Ffn, x: torch.Tensor, x_scales: torch.Tensor,
+                   layout: Optional[Layout], up: torch.Tensor, up_scales: torch.Tensor,
+                   down: torch.Tensor, down_scales: torch.Tensor,
+                   residual: Optional[torch.Tensor], y: torch.Tensor,
+                   pre: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """y = q(silu(x up_gate^T) * (x up^T)) down^T + residual on every expert's placed rows.
+
+    layout None: a dense block over num_tokens rows (num_experts == top_k == 1)."""
+    c, dev = "moe_expert_ffn", -1
+    rows = _rows(shape)
+    if rows is not None:
+        H, I = ffn.hidden, ffn.intermediate
+        rows = rows if layout is not None else shape.num_tokens
+        dev = _all(c, (("x", x, _E4M3, rows * H, True),
+                       ("x_scales", x_scales, _F32, rows * (H // 128), True),
+                       *_ffn_weights(shape, ffn, up, up_scales, down, down_scales, True, True),
+                       ("residual", residual, _BF16, rows * H, False),
+                       ("y", y, _BF16, rows * H, True), ("pre", pre, _BF16, rows * 2 * I, False),
+                       ("workspace", workspace, _BYTES, 0, False), *_segments(shape, layout)))
+    lay = None if layout is None else layout.c()
+    s, f = shape.c(), ffn.c()
+    ws = _workspace(_lib.moe_expert_ffn_workspace_size(ctypes.byref(s), ctypes.byref(f)),
+                    workspace, dev, stream)
+    _run(c, dev, stream, _lib.moe_expert_ffn, ctypes.byref(s), ctypes.byref(f), _ptr(x),
+         _ptr(x_scales), _maybe(lay), _ptr(up), _ptr(up_scales), _ptr(down), _ptr(down_scales),
+         _ptr(residual), _ptr(y), _ptr(pre), _ptr(ws), _nbytes(ws))
+
+
+def moe_expert_ffn_backward(shape: Shape, ffn: Ffn, grad_y: torch.Tensor,
+                            x: Optional[torch.Tensor], x_scales: Optional[torch.Tensor],
+                            layout: Optional[Layout], up: Optional[torch.Tensor],
+                            up_scales: Optional[torch.Tensor], down: Optional[torch.Tensor],
+                            down_scales: Optional[torch.Tensor], pre: torch.Tensor,
+                            grad_x: Optional[torch.Tensor], grad_up: Optional[torch.Tensor],
+                            grad_down: Optional[torch.Tensor],
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_expert_ffn; any of the three outputs may be None."""
+    c, dev = "moe_expert_ffn_backward", -1
+    rows = _rows(shape)
+    if rows is not None:
+        E, H, I = shape.num_experts, ffn.hidden, ffn.intermediate
+        rows = rows if layout is not None else shape.num_tokens
+        some = shape.num_tokens > 0
+        slopes = some and (grad_x is not None or grad_up is not None)
+        dev = _all(c, (("grad_y", grad_y, _BF16, rows * H, True),
+                       ("x", x, _E4M3, rows * H, grad_up is not None),
+                       ("x_scales", x_scales, _F32, rows * (H // 128), grad_up is not None),
+                       *_ffn_weights(shape, ffn, up, up_scales, down, down_scales,
+                                     some and grad_x is not None, slopes),
+                       ("pre", pre, _BF16, rows * 2 * I, True),
+                       ("grad_x", grad_x, _BF16, rows * H, False),
+                       ("grad_up", grad_up, _BF16, 2 * E * I * H, False),
+                       ("grad_down", grad_down, _BF16, E * I * H, False),
+                       ("workspace", workspace, _BYTES, 0, False), *_segments(shape, layout)))
+    lay = None if layout is None else layout.c()
+    s, f = shape.c(), ffn.c()
+    ws = _workspace(_lib.moe_expert_ffn_backward_workspace_size(ctypes.byref(s), ctypes.byref(f)),
+                    workspace, dev, stream)
+    _run(c, dev, stream, _lib.moe_expert_ffn_backward, ctypes.byref(s), ctypes.byref(f),
+         _ptr(grad_y), _ptr(x), _ptr(x_scales), _maybe(lay), _ptr(up), _ptr(up_scales),
+         _ptr(down), _ptr(down_scales), _ptr(pre), _ptr(grad_x), _ptr(grad_up), _ptr(grad_down),
+         _ptr(ws), _nbytes(ws))

@@ -1,31 +1,12 @@
 // capi_experts.hip -- argument checks of moe_experts.h, then launches on the
 // caller's stream.  No allocation, no synchronisation, no state.
 #include "moe_experts.h"
+#include "capi_check.h"
 #include "experts.h"
-#include "shape_check.h"
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-// present and aligned / absent or aligned
-bool rows_ok(const void* p) { return p && aligned16(p); }
-bool maybe_rows_ok(const void* p) { return aligned16(p); }
-
-moe_status from_hip(hipError_t e) {
-  if (e == hipErrorNotSupported) return MOE_ERR_UNSUPPORTED;  // the launchers' own limits
-  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
-}
-
-// A shape's receive rows.
-moe_status check_shape(const moe_shape* s, int* rows) {
-  int L;
-  int64_t n;
-  const moe_status st = moe::check_shape(s, &L, &n);
-  if (st != MOE_OK) return st;
-  if (n > MOE_MAX_EXPERT_ROWS) return MOE_ERR_UNSUPPORTED;
-  *rows = (int)n;
-  return MOE_OK;
-}
+using namespace moe::capi;
 
 moe_status check_linear(const moe_shape* s, const moe_linear* l, int* P) {
   if (!l || l->in_features <= 0 || l->out_features <= 0) return MOE_ERR_INVALID_ARG;
@@ -36,27 +17,6 @@ moe_status check_linear(const moe_shape* s, const moe_linear* l, int* P) {
   // a tile's rows are addressed with 32-bit byte offsets
   if (p > MOE_MAX_FEATURES || l->in_features > MOE_MAX_FEATURES) return MOE_ERR_UNSUPPORTED;
   *P = (int)p;
-  return MOE_OK;
-}
-
-moe_status segments(const moe_shape* s, const moe_layout* lay, int rows, moe::Segments* seg) {
-  if (lay) {
-    if (!lay->expert_counts || !lay->expert_offsets) return MOE_ERR_INVALID_ARG;
-    seg->counts = lay->expert_counts;
-    seg->offsets = lay->expert_offsets;
-  } else {
-    if (s->num_experts != 1 || s->top_k != 1) return MOE_ERR_INVALID_ARG;
-    if (s->num_tokens > rows) return MOE_ERR_INVALID_ARG;  // more tokens than rows
-    rows = s->num_tokens;
-    seg->counts = seg->offsets = nullptr;
-  }
-  seg->E = s->num_experts;
-  seg->L = s->num_experts / s->num_ranks;
-  seg->C = s->rank_capacity;
-  seg->rows = rows;
-  const int64_t pairs = (int64_t)s->num_tokens * s->top_k;
-  seg->pairs = (int)(pairs < rows ? pairs : rows);
-  if (seg->pairs == 0) seg->rows = 0;  // no segment, whatever the counts say
   return MOE_OK;
 }
 

@@ -1,0 +1,481 @@
+// expert_ffn.hip -- the experts' gated feed-forward block in 8 bits and its
+// gradient.
+//
+//   z = x Wu^T, h = silu(z1) z2, y = q(h) Wd^T
+//   gh = q(gy) Wd, gz = act'(z) gh, gx = q(gz) Wu, gWu = gz^T x, gWd = gy^T h
+//
+// with q the rounding of rows to e4m3 in blocks of 128 columns.  The products
+// with the weights are those of expert_product.h, one step one scale block:
+//   h      u = gate and up rows of 128 columns, v = token row, r = column of x
+//   gh, gx u = weight column, v = token row, r = weight row (weights transposed)
+// A tile has all columns of a scale block, so that rows are rounded to 8 bits where
+// they are made, from the fp32 sums, and the activation and its slope need no pass
+// of their own.  The weights' gradients are expert_matmul's, in bf16: they are
+// added up over many steps, and 2^-4 a factor would be their largest error by far.
+#include "expert_product.h"
+#include "ffn.h"
+#include "quantize.h"
+
+namespace moe {
+
+namespace {
+
+// 256 columns of u by 256 token rows in two steps of LDS (Codes), or by 128 in
+// three.
+using ShortCodes = Config<2, 4, 8, 2>;
+template <class C>
+constexpr int kStages = C::kTv == 4 ? 2 : 3;
+
+// ---------------------------------------------------------------------------
+// Forward: h
+// ---------------------------------------------------------------------------
+struct UpParams {
+  Segments seg;
+  const uint8_t* x;
+  const float* x_scales;
+  const uint8_t* up;
+  const float* up_scales;
+  uint16_t* pre;
+  uint8_t* h;
+  float* h_scales;
+  int H, I;
+};
+
+// The gated activation on the accumulators, then rows of 128 columns to 8 bits.
+// A wave has 64 of the columns; the largest magnitudes meet in LDS.
+template <class C, class Product>
+__device__ __forceinline__ void finish_up(Product& prod, const UpParams& p, const Tile& t,
+                                          int wave, uint32_t* s_largest) {
+  using Cols = Columns<C, kActSwiglu>;
+  static_assert(Cols::kTile == kFp8Block, "a tile is one block of columns");
+  const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
+  const int col0 = t.n * kFp8Block + wu * Cols::kWave + (lane >> 4) * 8;
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int row = (v * C::kWv + wv) * 16 + (lane & 15), m = t.m0 + row;
+    uint32_t largest = 0;
+#pragma unroll
+    for (int a = 0; a < Cols::kPairs; ++a) {
+      float z[8], up[8];
+      prod.eight(z, a, v);
+      prod.eight(up, a + Cols::kPairs, v);
+      if (p.pre && m < t.end) {
+        uint16_t* pre = p.pre + (size_t)m * (2 * p.I) + col0 + a * 32;
+        store8(pre, z);
+        store8(pre + p.I, up);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z[i] = z[i] * sigmoid_f32(z[i]) * up[i];
+        largest = max(largest, magnitude(z[i]));
+        prod.acc[2 * a + i / 4][v][i % 4] = z[i];
+      }
+    }
+    largest = max_over_rows(largest);
+    if (lane < 16) s_largest[wu * C::kBv + row] = largest;
+  }
+  lds_barrier();
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int row = (v * C::kWv + wv) * 16 + (lane & 15), m = t.m0 + row;
+    if (m >= t.end) continue;
+    uint32_t largest = 0;
+#pragma unroll
+    for (int w = 0; w < C::kWu; ++w) largest = max(largest, s_largest[w * C::kBv + row]);
+    const BlockScale block(largest);
+#pragma unroll
+    for (int a = 0; a < Cols::kPairs; ++a) {
+      float h[8];
+      prod.eight(h, a, v);
+      *reinterpret_cast<uint2*>(p.h + (size_t)m * p.I + col0 + a * 32) = block.codes(h);
+    }
+    if (wu == 0 && lane < 16) p.h_scales[(size_t)m * (p.I / kFp8Block) + t.n] = block.scale;
+  }
+}
+
+template <class C>
+constexpr int kUpLds = Fp8Product<C, kStages<C>>::kLds + C::kWu * C::kBv * 4;
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+ffn_up_kernel(UpParams p, int ntiles) {
+  using Product = Fp8Product<C, kStages<C>>;
+  using Cols = Columns<C, kActSwiglu>;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+  const int kb = p.H / kFp8Block, ib = p.I / kFp8Block;
+  const uint32_t ld = (uint32_t)p.H;
+  const int rows = min(C::kBv, t.end - t.m0);
+  Product prod;
+  const char* ap[Product::A::kLoads];
+  weight_loads<C, kActSwiglu>(
+      prod.a, ap,
+      reinterpret_cast<const char*>(p.up) + ((size_t)t.e * 2 * p.I + t.n * Cols::kTile) * ld, wave,
+      p.I, p.I - t.n * Cols::kTile, ld);
+  prod.b.init(wave, ld, rows);
+  const float* scale =
+      lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
+                : p.up_scales + ((size_t)t.e * 2 * ib + t.n + (lane % 2 == 1 ? ib : 0)) * kb;
+  prod.run_rows(smem, wave, ap, reinterpret_cast<const char*>(p.x) + (size_t)t.m0 * ld, scale, kb,
+                rows);
+  finish_up<C>(prod, p, t, wave, reinterpret_cast<uint32_t*>(smem + Product::kLds));
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+// Placed rows of grad_y to 8 bits and of x to bf16 (code times scale, half a bf16
+// step off; NULL: not wanted): a stream, 16 rows a block.
+constexpr int kPrepareRows = 16, kPrepareThreads = 256;
+
+struct PrepareParams {
+  Segments seg;
+  const uint16_t* grad_y;
+  uint8_t* gy;
+  float* gy_scales;
+  const uint8_t* x;
+  const float* x_scales;
+  uint16_t* wide_x;
+  int H;
+};
+
+__global__ void __launch_bounds__(kPrepareThreads)
+ffn_prepare_kernel(PrepareParams p) {
+  Tile t;
+  if (!find_tile<kPrepareRows>(p.seg, 1, blockIdx.x, t)) return;
+  const int rows = min(kPrepareRows, t.end - t.m0), units = p.H / 8;
+  // units per row are a multiple of 16: the 16 lanes of a scale block stay together
+  for (int i = threadIdx.x; i < rows * units; i += kPrepareThreads) {
+    const size_t at = (size_t)t.m0 * p.H + (size_t)i * 8;
+    float v[8];
+    load8(v, p.grad_y + at);
+    uint32_t largest = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) largest = max(largest, magnitude(v[j]));
+    const BlockScale block(max_over_16(largest));
+    *reinterpret_cast<uint2*>(p.gy + at) = block.codes(v);
+    if (threadIdx.x % 16 == 0) p.gy_scales[at / kFp8Block] = block.scale;
+    if (p.wide_x) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p.x + at);
+      const float s = p.x_scales[at / kFp8Block];
+      e4m3x4_to_f32(q.x, v);
+      e4m3x4_to_f32(q.y, v + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= s;
+      store8(p.wide_x + at, v);
+    }
+  }
+}
+
+// h alone, where only the second weight's gradient is wanted.
+__global__ void __launch_bounds__(kPrepareThreads)
+ffn_hidden_kernel(Segments seg, const uint16_t* pre, uint16_t* h, int I) {
+  Tile t;
+  if (!find_tile<kPrepareRows>(seg, 1, blockIdx.x, t)) return;
+  const int rows = min(kPrepareRows, t.end - t.m0), units = I / 8;
+  for (int i = threadIdx.x; i < rows * units; i += kPrepareThreads) {
+    const size_t m = t.m0 + i / units;
+    const int c = i % units * 8;
+    float g[8], u[8];
+    load8(g, pre + m * (2 * I) + c);
+    load8(u, pre + m * (2 * I) + I + c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = g[j] * sigmoid_f32(g[j]) * u[j];
+    store8(h + m * I + c, g);
+  }
+}
+
+struct SlopeParams {
+  Segments seg;
+  const uint8_t* gy;
+  const float* gy_scales;
+  const uint8_t* down;
+  const float* down_scales;
+  const uint16_t* pre;
+  uint8_t* gz;         // rows of 2I in 8 bits, or NULL
+  float* gz_scales;
+  uint16_t* wide_gz;   // the same in bf16, or NULL
+  uint16_t* h;         // rows of I in bf16, or NULL
+  int H, I;
+};
+
+// The slope of the activation on the accumulators; a wave has all 128 columns of a
+// scale block, of the gate's and of the up half's gradient.
+template <class C, class Product>
+__device__ __forceinline__ void finish_slope(const Product& prod, const SlopeParams& p,
+                                             const Tile& t, int wave) {
+  constexpr int kPairs = C::kTu / 2;
+  static_assert(kPairs * 32 == kFp8Block, "a wave's columns are one block");
+  const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
+  const int col0 = (t.n * C::kWu + wu) * kFp8Block;
+  if (col0 >= p.I) return;
+  const int P = 2 * p.I, pb = P / kFp8Block;
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int row = (v * C::kWv + wv) * 16 + (lane & 15), m = t.m0 + row;
+    const bool there = m < t.end;
+    const size_t at = (size_t)(there ? m : t.m0) * P;
+    float dg[kPairs][8], du[kPairs][8];
+    uint32_t largest_g = 0, largest_u = 0;
+#pragma unroll
+    for (int a = 0; a < kPairs; ++a) {
+      const int col = col0 + Product::column(a);
+      float gh[8], g[8], u[8], h[8];
+      prod.eight(gh, a, v);
+      load8(g, p.pre + at + col);
+      load8(u, p.pre + at + p.I + col);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float s = sigmoid_f32(g[i]);
+        const float silu = g[i] * s;
+        dg[a][i] = gh[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+        du[a][i] = gh[i] * silu;
+        h[i] = silu * u[i];
+        largest_g = max(largest_g, magnitude(dg[a][i]));
+        largest_u = max(largest_u, magnitude(du[a][i]));
+      }
+      if (!there) continue;
+      if (p.h) store8(p.h + (size_t)m * p.I + col, h);
+      if (p.wide_gz) {
+        store8(p.wide_gz + at + col, dg[a]);
+        store8(p.wide_gz + at + p.I + col, du[a]);
+      }
+    }
+    if (!p.gz) continue;
+    const BlockScale gate(max_over_rows(largest_g)), up(max_over_rows(largest_u));
+    if (!there) continue;
+#pragma unroll
+    for (int a = 0; a < kPairs; ++a) {
+      const int col = col0 + Product::column(a);
+      *reinterpret_cast<uint2*>(p.gz + at + col) = gate.codes(dg[a]);
+      *reinterpret_cast<uint2*>(p.gz + at + p.I + col) = up.codes(du[a]);
+    }
+    if (lane < 16) {
+      float* scales = p.gz_scales + (size_t)m * pb + col0 / kFp8Block;
+      scales[0] = gate.scale;
+      scales[pb / 2] = up.scale;
+    }
+  }
+}
+
+// The product with transposed weights, rows of `cols` columns: sums over `red`
+// weight rows.
+template <class C, class Product>
+__device__ __forceinline__ void transposed_product(Product& prod, char* smem, const Tile& t,
+                                                   int wave, const uint8_t* rows_codes,
+                                                   const float* row_scales, const uint8_t* weight,
+                                                   const float* weight_scales, int red, int cols) {
+  const int lane = lane_id(), rb = red / kFp8Block, cb = cols / kFp8Block, n0 = t.n * C::kBu;
+  const int rows = min(C::kBv, t.end - t.m0);
+  const char* ap[Product::A::kLoads];
+#pragma unroll
+  for (int i = 0; i < Product::A::kLoads; ++i)
+    ap[i] = reinterpret_cast<const char*>(weight) + (size_t)t.e * red * cols + n0;
+  prod.a_step = (size_t)kFp8Block * cols;
+  prod.a.init(wave, (uint32_t)cols, min(C::kBu, cols - n0));
+  prod.b.init(wave, (uint32_t)red, rows);
+  // a wave's columns lie in one block of scales; past the last column any will do
+  static_assert(C::kTu * 16 <= kFp8Block, "one scale a wave");
+  const int block = min(n0 + wave % C::kWu * (C::kTu * 16), cols - 1) / kFp8Block;
+  const float* scale =
+      lane < 32 ? row_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * rb
+                : weight_scales + (size_t)t.e * rb * cb + block;
+  prod.scale_step = lane < 32 ? 1 : cb;
+  prod.run_rows(smem, wave, ap, reinterpret_cast<const char*>(rows_codes) + (size_t)t.m0 * red,
+                scale, rb, rows);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+ffn_slope_kernel(SlopeParams p, int ntiles) {
+  using Product = Fp8Product<C, kStages<C>, true>;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  Product prod;
+  transposed_product<C>(prod, smem, t, wave, p.gy, p.gy_scales, p.down, p.down_scales, p.H, p.I);
+  finish_slope<C>(prod, p, t, wave);
+}
+
+struct RowGradParams {
+  Segments seg;
+  const uint8_t* gz;
+  const float* gz_scales;
+  const uint8_t* up;
+  const float* up_scales;
+  uint16_t* grad_x;
+  int H, I;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+ffn_grad_x_kernel(RowGradParams p, int ntiles) {
+  using Product = Fp8Product<C, kStages<C>, true>;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  Product prod;
+  transposed_product<C>(prod, smem, t, wave, p.gz, p.gz_scales, p.up, p.up_scales, 2 * p.I, p.H);
+  const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int m = t.m0 + (v * C::kWv + wv) * 16 + (lane & 15);
+#pragma unroll
+    for (int a = 0; a < C::kTu / 2; ++a) {
+      const int col = t.n * C::kBu + wu * (C::kTu * 16) + Product::column(a);
+      float o[8];
+      prod.eight(o, a, v);
+      if (m < t.end && col < p.H) store8(p.grad_x + (size_t)m * p.H + col, o);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+// u: columns along u in all, cols of them a tile
+template <class C, auto KERNEL, int LDS, class Params>
+hipError_t launch_product(const Params& p, int u, int cols, hipStream_t st) {
+  const int ntiles = (u + cols - 1) / cols;
+  const int64_t grid = tile_bound(p.seg, C::kBv, ntiles);
+  if (!launchable(grid, C::kThreads)) return hipErrorNotSupported;
+  const hipError_t e = allow_lds<KERNEL, LDS>();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(KERNEL, dim3((unsigned)grid), dim3(C::kThreads), LDS, st, p, ntiles);
+  return hipGetLastError();
+}
+
+size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Pieces of a workspace one after the other.
+struct Carver {
+  char* at;
+  template <class T>
+  T* take(size_t n) {
+    T* p = reinterpret_cast<T*>(at);
+    at += round_up(n * sizeof(T));
+    return p;
+  }
+};
+
+// Products of up to u columns can be launched at all (the smallest tile has 128 x
+// 128 of them).
+bool launchable_columns(const Segments& s, int u) {
+  return launchable(tile_bound(s, 128, (u + 127) / 128), 512);
+}
+
+}  // namespace
+
+size_t expert_ffn_workspace(int rows, int pairs, int E, int H, int I) {
+  if (pairs == 0) return 0;
+  return round_up((size_t)rows * I) + round_up((size_t)rows * (I / kFp8Block) * 4);
+}
+
+hipError_t launch_expert_ffn(const FfnParams& p, hipStream_t st) {
+  if (!launchable_columns(p.seg, p.I) || !launchable_columns(p.seg, p.H))
+    return hipErrorNotSupported;
+  Carver ws{static_cast<char*>(p.workspace)};
+  uint8_t* h = ws.take<uint8_t>((size_t)p.seg.rows * p.I);
+  float* h_scales = ws.take<float>((size_t)p.seg.rows * (p.I / kFp8Block));
+  const UpParams up{p.seg, p.x, p.x_scales, p.up, p.up_scales, p.pre, h, h_scales, p.H, p.I};
+  hipError_t e = large_codes(p.seg, 2 * p.I)
+                     ? launch_product<Codes, ffn_up_kernel<Codes>, kUpLds<Codes>>(up, p.I, 128, st)
+                     : launch_product<ShortCodes, ffn_up_kernel<ShortCodes>, kUpLds<ShortCodes>>(
+                           up, p.I, 128, st);
+  if (e != hipSuccess) return e;
+  MatmulParams down{};
+  down.seg = p.seg;
+  down.x = h;
+  down.x_scales = h_scales;
+  down.weight = p.down;
+  down.weight_scales = p.down_scales;
+  down.residual = p.residual;
+  down.y = p.y;
+  down.K = p.I;
+  down.F = down.P = p.H;
+  down.act = kActNone;
+  return launch_expert_matmul(down, true, st);
+}
+
+size_t expert_ffn_grad_workspace(int rows, int H, int I) {
+  const size_t n = rows, P = 2 * (size_t)I;
+  return round_up(n * H) + round_up(n * (H / kFp8Block) * 4) + round_up(n * P) +
+         round_up(n * (P / kFp8Block) * 4) + round_up(n * P * 2) + round_up(n * I * 2) +
+         round_up(n * H * 2);
+}
+
+hipError_t launch_expert_ffn_grad(const FfnGradParams& p, hipStream_t st) {
+  const Segments& seg = p.seg;
+  const int P = 2 * p.I, hb = p.H / kFp8Block, pb = P / kFp8Block;
+  if (!launchable_columns(seg, p.I) || !launchable_columns(seg, p.H) ||
+      (int64_t)seg.E * hb * pb > INT32_MAX ||
+      !launchable(tile_bound(seg, kPrepareRows, 1), kPrepareThreads))
+    return hipErrorNotSupported;
+  const size_t n = seg.rows;
+  Carver ws{static_cast<char*>(p.workspace)};
+  uint8_t* gy = ws.take<uint8_t>(n * p.H);
+  float* gy_scales = ws.take<float>(n * hb);
+  uint8_t* gz = ws.take<uint8_t>(n * P);
+  float* gz_scales = ws.take<float>(n * pb);
+  uint16_t* wide_gz = ws.take<uint16_t>(n * P);
+  uint16_t* h = ws.take<uint16_t>(n * p.I);
+  uint16_t* wide_x = ws.take<uint16_t>(n * p.H);
+  hipError_t e = hipSuccess;
+  if (seg.pairs > 0 && !p.grad_x && !p.grad_up) {
+    hipLaunchKernelGGL(ffn_hidden_kernel, dim3((unsigned)tile_bound(seg, kPrepareRows, 1)),
+                       dim3(kPrepareThreads), 0, st, seg, p.pre, h, p.I);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  } else if (seg.pairs > 0) {
+    const PrepareParams prepare{seg,  p.grad_y, gy, gy_scales, p.x, p.x_scales,
+                                p.grad_up ? wide_x : nullptr, p.H};
+    hipLaunchKernelGGL(ffn_prepare_kernel, dim3((unsigned)tile_bound(seg, kPrepareRows, 1)),
+                       dim3(kPrepareThreads), 0, st, prepare);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const SlopeParams slope{seg,   gy,
+                            gy_scales, p.down,
+                            p.down_scales, p.pre,
+                            p.grad_x ? gz : nullptr, gz_scales,
+                            p.grad_up ? wide_gz : nullptr, p.grad_down ? h : nullptr,
+                            p.H,   p.I};
+    constexpr int kLds = Fp8Product<Codes, kStages<Codes>, true>::kLds;
+    constexpr int kFewLds = Fp8Product<ShortCodes, kStages<ShortCodes>, true>::kLds;
+    e = large_codes(seg, p.I)
+            ? launch_product<Codes, ffn_slope_kernel<Codes>, kLds>(slope, p.I, 256, st)
+            : launch_product<ShortCodes, ffn_slope_kernel<ShortCodes>, kFewLds>(slope, p.I, 256, st);
+    if (e != hipSuccess) return e;
+    if (p.grad_x) {
+      const RowGradParams row{seg, gz, gz_scales, p.up, p.up_scales, p.grad_x, p.H, p.I};
+      e = large_codes(seg, p.H)
+              ? launch_product<Codes, ffn_grad_x_kernel<Codes>, kLds>(row, p.H, 256, st)
+              : launch_product<ShortCodes, ffn_grad_x_kernel<ShortCodes>, kFewLds>(row, p.H, 256, st);
+      if (e != hipSuccess) return e;
+    }
+  }
+  MatmulGradParams w{};
+  w.seg = seg;
+  w.act = kActNone;
+  if (p.grad_up) {
+    w.grad_y = wide_gz;
+    w.x = wide_x;
+    w.grad_weight = p.grad_up;
+    w.K = p.H;
+    w.F = w.P = P;
+    if ((e = launch_expert_matmul_grad(w, st)) != hipSuccess) return e;
+  }
+  if (p.grad_down) {
+    w.grad_y = p.grad_y;
+    w.x = h;
+    w.grad_weight = p.grad_down;
+    w.K = p.I;
+    w.F = w.P = p.H;
+    e = launch_expert_matmul_grad(w, st);
+  }
+  return e;
+}
+
+}  // namespace moe

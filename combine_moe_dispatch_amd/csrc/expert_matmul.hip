@@ -24,257 +24,15 @@
 // power they draw (4096 tokens, 1.75 TFLOP in 1.51 ms back to back, 1.64 on
 // average under a profiler; as one dense product 1.36 ms against 1.29 of the
 // library's).
-#include <atomic>
 #include <type_traits>
 
-#include "expert_tile.h"
+#include "expert_product.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-// ---------------------------------------------------------------------------
-// The tile product
-// ---------------------------------------------------------------------------
-// WU x WV waves of TU x TV fragments of 16 x 16.  A wave's fragments lie side
-// by side along u and kWv apart along v, so that the rows of a part tile are
-// spread over all waves.
-template <int WU, int WV, int TU, int TV>
-struct Config {
-  static constexpr int kWu = WU, kWv = WV, kTu = TU, kTv = TV;
-  static constexpr int kWaves = WU * WV, kThreads = kWaves * kWave;
-  static constexpr int kBu = WU * TU * 16, kBv = WV * TV * 16;
-};
-
-//
-// Four waves: with one wave to a SIMD each holds 128 x 128 of a 256 x 256 tile
-// and reads a quarter less from LDS per product than eight waves of 128 x 64
-// (prefill of 4096 tokens 1.62 against 1.73 ms; in two teams of four that
-// read and multiply in turns 1.80 ms, with 32 x 32 x 16 products 1.84 ms).
-// The matrix units draw the chip's power, so what counts is less work around
-// them rather than fewer idle cycles: the clock falls as those go.
-template <class C, bool AT, bool BT>
-struct TileProduct {
-  using A = OperandTile<C::kBu, C::kWaves, AT, true>;
-  using B = OperandTile<C::kBv, C::kWaves, BT, false>;
-  static constexpr int kStage = A::kBytes + B::kBytes;
-  static constexpr int kLds = 2 * kStage;
-  static constexpr int kLoads = A::kLoads + B::kLoads;
-  struct Fragments {
-    bf16x8_t a[C::kTu], b[C::kTv];
-  };
-  A a;
-  B b;
-  f32x4_t acc[C::kTu][C::kTv];
-  typename A::template Reader<C::kTu> ra;
-  typename B::template Reader<C::kTv> rb;
-
-  // A tile whose last quarters have no rows (only where B's rows run along r)
-  // leaves out their products and B's loads of them: PART is how many of the
-  // fragments along v a wave has to do, in quarters of kTv.
-  template <int PART>
-  static constexpr int kPartLoads = A::kLoads + B::kLoads * PART / C::kTv;
-
-  // Fragment i (of PART + kTu) of part k of the step at lds.
-  template <int PART, bool TAIL>
-  __device__ __forceinline__ void read(Fragments& f, int i, uint32_t lds, int k, int left) const {
-    if (i < PART)
-      f.b[i] = rb.template frag<TAIL>(lds + A::kBytes, i * (BT ? 1 : C::kWv), k, left);
-    else
-      f.a[i - PART] = ra.template frag<TAIL>(lds, i - PART, k, left);
-  }
-  template <int PART, bool TAIL>
-  __device__ __forceinline__ void read_all(Fragments& f, uint32_t lds, int k, int left) const {
-#pragma unroll
-    for (int i = 0; i < PART + C::kTu; ++i) read<PART, TAIL>(f, i, lds, k, left);
-  }
-
-  // acc += f, row of fragments by row, with before(u) in front of row u: what
-  // it issues runs beside the products.
-  template <int PART, class Before>
-  __device__ __forceinline__ void multiply(const Fragments& f, Before before) {
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u) {
-      before(u);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int v = 0; v < PART; ++v) mfma_in_place(acc[u][v], f.a[u], f.b[v]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u)
-#pragma unroll
-      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
-  }
-
-  // A tile's operands: ap[i] is where load i of this wave starts in A (weight
-  // rows of a gated layer lie in two places), bp in B; lda, ldb are the
-  // operands' row pitches in bytes, red > 0 the positions along r.
-  const char* ap[A::kLoads];
-  const char* bp;
-  uint32_t lda, ldb;
-  int red, wave;
-  uint32_t lds;
-
-  __device__ __forceinline__ void setup(char* smem, int wave_) {
-    wave = wave_;
-    lds = lds_address(smem);
-    ra.init(wave % C::kWu * C::kTu * 16);
-    rb.init(wave / C::kWu * 16, C::kWv);
-  }
-  __device__ __forceinline__ int steps() const { return (red + kStep - 1) / kStep; }
-  // The next step's load i, and all of them.
-  template <bool TAIL>
-  __device__ __forceinline__ void load(int i, uint32_t to) {
-    const int rest = red % kStep;
-    if (i < A::kLoads)
-      a.template load<TAIL>(i, to, wave, ap[i], lda, rest);
-    else if (i < kLoads)
-      b.template load<TAIL>(i - A::kLoads, to + A::kBytes, wave, bp, ldb, rest);
-  }
-  __device__ __forceinline__ void advance() {
-#pragma unroll
-    for (int i = 0; i < A::kLoads; ++i) ap[i] += AT ? (size_t)kStep * lda : (size_t)kStep * 2;
-    bp += BT ? (size_t)kStep * ldb : (size_t)kStep * 2;
-  }
-  template <int PART>
-  __device__ __forceinline__ void start(uint32_t to, bool full) {
-    if (full) {
-#pragma unroll
-      for (int i = 0; i < kPartLoads<PART>; ++i) load<false>(i, to);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPartLoads<PART>; ++i) load<true>(i, to);
-    }
-    advance();
-  }
-  // Start the first two steps of a tile.  No wave may still read LDS.
-  template <int PART>
-  __device__ __forceinline__ void begin() {
-    const int whole = red / kStep;
-    start<PART>(lds, whole > 0);
-    if (steps() > 1) start<PART>(lds + kStage, whole > 1);
-  }
-
-  // The tile that begin() has started.  Afterwards LDS is free again.  behind:
-  // stores that this wave has started since (0, or kStores at least).
-  template <int PART>
-  __device__ __forceinline__ void run(int behind) {
-    constexpr int kLoads = kPartLoads<PART>;
-    constexpr int kBehind = C::kTv * C::kTu / 2;
-    static_assert(kLoads + kBehind < 64, "counted by the hardware");
-    static_assert(kParts == 2, "the parts are written out");
-    clear();
-    uint32_t here = lds, next = lds + kStage;
-    const int steps = this->steps(), whole = red / kStep;
-    const int rest = red - (steps - 1) * kStep;  // positions of the last step
-    // Every wave's reads of `here` are in registers and its loads of `next` in
-    // LDS: `here` may be filled again and `next` be read.
-    auto meet = [&] {
-      wait_lds();
-      wait_vm<0>();
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-    };
-    auto turn = [&] {
-      const uint32_t h = here;
-      here = next;
-      next = h;
-    };
-    constexpr int kReads = (2 * (C::kTu + PART) + C::kTu - 1) / C::kTu;  // in the first rows
-    constexpr int kStarts = (kLoads + C::kTu - 1) / C::kTu;
-    auto reading = [&](Fragments& f, uint32_t lds, int k, int u) {
-#pragma unroll
-      for (int i = u * kReads; i < (u + 1) * kReads; ++i)
-        if (i < C::kTu + PART) read<PART, false>(f, i, lds, k, rest);
-    };
-    const auto nothing = [](int) {};
-    Fragments f0, f1;
-    if (steps > 1 && behind > 0)
-      wait_vm<kLoads + kBehind>();
-    else if (steps > 1)
-      wait_vm<kLoads>();
-    else
-      wait_vm<0>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (steps > 1)
-      read_all<PART, false>(f0, here, 0, rest);
-    else
-      read_all<PART, true>(f0, here, 0, rest);
-    // Half a step is multiplied while the next half is read, the second half
-    // behind the barrier, so that the matrix units have work on both sides.
-    for (int t = 0; t + 2 < whole; ++t) {
-      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
-      meet();
-      multiply<PART>(f1, [&](int u) {
-        reading(f0, next, 0, u);
-#pragma unroll
-        for (int i = u * kStarts; i < (u + 1) * kStarts; ++i)
-          if (i < kLoads) load<false>(i, here);
-      });
-      advance();
-      turn();
-    }
-    if (whole < steps && steps > 2) {  // the step whose loads are the short ones
-      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
-      meet();
-      start<PART>(here, false);
-      multiply<PART>(f1, [&](int u) { reading(f0, next, 0, u); });
-      turn();
-    }
-    if (steps > 1) {
-      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
-      meet();
-      multiply<PART>(f1, nothing);
-      read_all<PART, true>(f0, next, 0, rest);
-      turn();
-    }
-    // the second half of the last step may have no positions (a weight gradient
-    // over 256 rows an expert 3% less)
-    if (rest > kPart) read_all<PART, true>(f1, here, 1, rest);
-    multiply<PART>(f0, nothing);
-    wait_lds();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (rest > kPart) multiply<PART>(f1, nothing);
-    mfma_results();
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u)
-#pragma unroll
-      for (int v = 0; v < C::kTv; ++v) mfma_result(acc[u][v]);
-  }
-
-  // A tile of `rows` along v, from its first load on.
-  template <int PART>
-  __device__ __forceinline__ void begin_and_run() {
-    static_assert(!BT, "the front of a transposed operand's tile is not its first columns");
-    begin<PART>();
-    run<PART>(0);
-  }
-  __device__ __forceinline__ void begin_and_run(int rows) {
-    if (rows > C::kBv * 3 / 4)
-      begin_and_run<C::kTv>();
-    else if (rows > C::kBv / 2)
-      begin_and_run<C::kTv * 3 / 4>();
-    else if (rows > C::kBv / 4)
-      begin_and_run<C::kTv / 2>();
-    else
-      begin_and_run<C::kTv / 4>();
-  }
-
-  // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours
-  // along u from a * 32 + (lane >> 4) * 8 on, of the fragment's row lane & 15.
-  __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
-  }
-};
 
 // ---------------------------------------------------------------------------
 // The product for few rows an expert, where the weights' way from memory is
@@ -401,141 +159,6 @@ struct StreamProduct {
 };
 
 // ---------------------------------------------------------------------------
-// The same for e4m3 operands with a scale per 128 values along r: one step is
-// one block of 128, whose products are summed by one 16 x 16 x 128 matrix
-// instruction per fragment and then scaled in fp32, sx of the token times sw
-// of the 128 weight rows.  A row of a step is 128 bytes, as in the bf16
-// product, so the tiles in LDS are the same; the chunks of a fragment are
-// taken in an order of their own, equal for both operands, which a sum does
-// not notice.  Eight waves, two on every SIMD: one scales while the other
-// multiplies.
-//
-// The instruction's own sum has fewer bits than fp32: of 8 neighbouring columns
-// it cuts every product below 2^-13 of the largest (measured; the 16 x 16 x 32
-// instruction does the same), so a sum is off by less than 2^-10 of the groups'
-// largest products (2.5 2^-13 at most in 10^5 sums of random codes, 2^-19 of the
-// magnitudes in the mean of normal ones).  Both factors of a product were
-// rounded to 2^-4 before, and exact sums would need the codes widened to bf16, at
-// half the rate.
-// ---------------------------------------------------------------------------
-template <class C, int STAGES>
-struct Fp8Product {
-  using A = OperandTile<C::kBu, C::kWaves, false, true>;
-  using B = OperandTile<C::kBv, C::kWaves, false, false>;
-  static constexpr int kScales = C::kWaves * 256;  // one dword a lane
-  static_assert(C::kBv == C::kWaves * 32, "a wave brings in the scales of 32 rows");
-  static constexpr int kStage = A::kBytes + B::kBytes + kScales;
-  static constexpr int kLds = STAGES * kStage;
-  static constexpr int kRows = 4;  // of fragments multiplied at a time
-  A a;
-  B b;
-  f32x4_t acc[C::kTu][C::kTv];
-  typename A::template Reader<C::kTu> ra;
-  typename B::template Reader<C::kTv> rb;
-
-  template <class R>
-  static __device__ __forceinline__ i32x8_t frag(const R& r, uint32_t lds, int n) {
-    union {
-      bf16x8_t h[2];
-      i32x8_t v;
-    } u;
-    u.h[0] = r.template frag<false>(lds, n, 0, 0);
-    u.h[1] = r.template frag<false>(lds, n, 1, 0);
-    return u.v;
-  }
-
-  // PART: as in TileProduct.  blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
-  // 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of the weight rows
-  // behind the first and the second half of the wave's fragments.  (A plain
-  // load of them would wait for every load to LDS before it.)  rows: how many
-  // the tile has.
-  template <int PART>
-  __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
-                                      const char* bp, const float* scale, int blocks, int rows) {
-    constexpr int kRowLoads = B::kLoads * PART / C::kTv;
-    constexpr int kLoads = A::kLoads + kRowLoads + 1;
-    ra.init(wave % C::kWu * C::kTu * 16);
-    rb.init(wave / C::kWu * 16);
-#pragma unroll
-    for (int u = 0; u < C::kTu; ++u)
-#pragma unroll
-      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
-    const uint32_t lds = lds_address(smem), lds_end = lds + kLds;
-    uint32_t fill = lds, here = lds;
-    auto after = [&](uint32_t slot) { return slot + kStage == lds_end ? lds : slot + kStage; };
-    auto start = [&] {
-#pragma unroll
-      for (int i = 0; i < A::kLoads; ++i) {
-        a.template load<false>(i, fill, wave, ap[i], 0, 0);
-        ap[i] += 128;
-      }
-#pragma unroll
-      for (int i = 0; i < kRowLoads; ++i)
-        b.template load<false>(i, fill + A::kBytes, wave, bp, 0, 0);
-      load4_to_lds(fill + A::kBytes + B::kBytes + wave * 256, scale);
-      bp += 128;
-      scale += 1;
-      fill = after(fill);
-    };
-    for (int t = 0; t < STAGES - 1 && t < blocks; ++t) start();
-    // the fragments of this wave that hold rows at all
-    const int wv = wave / C::kWu;
-    const int nv = min((rows - wv * 16 + C::kWv * 16 - 1) / (C::kWv * 16), C::kTv);
-    // 32 rows of scales every 256 bytes, this wave's two behind its own 32
-    const uint32_t scales = A::kBytes + B::kBytes;
-    const uint32_t sw_at = scales + wave * 256 + 128;
-    const uint32_t sx_at = scales + wv / 2 * 256 + wv % 2 * 64 + (lane_id() & 15) * 4;
-    static_assert(C::kWv % 2 == 0, "a fragment's scales lie 256 bytes per two fragments on");
-    auto lds_float = [](uint32_t p) {
-      return *(const __attribute__((address_space(3))) float*)(uintptr_t)p;
-    };
-    for (int t = 0; t < blocks; ++t) {
-      if (t + STAGES - 1 <= blocks)
-        wait_vm<(STAGES - 2) * kLoads>();
-      else
-        wait_vm<0>();
-      wait_lds();  // this wave has read the step before out
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      if (t + STAGES - 1 < blocks) start();
-      if (nv > 0) {
-        const float sw[2] = {lds_float(here + sw_at), lds_float(here + sw_at + 4)};
-#pragma unroll
-        for (int u0 = 0; u0 < C::kTu; u0 += kRows) {
-          i32x8_t fa[kRows];
-#pragma unroll
-          for (int u = 0; u < kRows; ++u) fa[u] = frag(ra, here, u0 + u);
-#pragma unroll
-          for (int v = 0; v < PART; ++v) {
-            if (v >= nv) break;
-            const i32x8_t fb = frag(rb, here + A::kBytes, v * C::kWv);
-            const float sx = lds_float(here + sx_at + v * C::kWv / 2 * 256);
-            f32x4_t part[kRows];
-#pragma unroll
-            for (int u = 0; u < kRows; ++u)
-              part[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[u], fb, f32x4_t{}, 0,
-                                                                         0, 0, 0, 0, 0);
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-              const float s = sx * sw[u0 + u < C::kTu / 2 ? 0 : 1];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[u0 + u][v][i] = fmaf(part[u][i], s, acc[u0 + u][v][i]);
-            }
-          }
-        }
-      }
-      here = after(here);
-    }
-  }
-
-  __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
-  }
-};
-
-// ---------------------------------------------------------------------------
 // gz = grad_y * act'(pre) to bf16, and its column sums in fp32 (summed before
 // that rounding).  A stream: a lane owns 8 columns (of the gate and of the up
 // half), a block 4 x 512 columns of every split's rows, four rows on their way
@@ -547,16 +170,6 @@ struct Fp8Product {
 // off by 2.3e-3 of their size, 1.7e-3 with the outputs' rounding alone.
 // ---------------------------------------------------------------------------
 constexpr int kActRows = 4;
-
-__device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
@@ -645,37 +258,6 @@ int act_splits(int pairs, int E, int F) {
   const int64_t blocks = (int64_t)E * ((F + 511) / 512);
   const int64_t want = (2048 + blocks - 1) / blocks, most = pairs / E / 16 + 1;
   return (int)(want < most ? want : most);
-}
-
-// y (and pre): u runs over weight rows; a gated layer's wave takes half of its
-// fragments from the gate rows and half from the up rows of the same columns.
-template <class C, int ACT>
-struct Columns {
-  static constexpr bool kGated = ACT == kActSwiglu;
-  static constexpr int kPairs = (kGated ? C::kTu / 2 : C::kTu) / 2;  // along the output's columns
-  static constexpr int kWave = kPairs * 32;                          // output columns of a wave
-  static constexpr int kTile = kWave * C::kWu;                       // and of the tile
-};
-
-// This wave's loads of weight rows: w is the first of the tile's (gate) rows,
-// cols how many columns are left from there, ld the bytes of a row.
-template <class C, int ACT, class A>
-__device__ __forceinline__ void weight_loads(A& a, const char* (&ap)[A::kLoads], const char* w,
-                                             int wave, int F, int cols, uint32_t ld) {
-  using Cols = Columns<C, ACT>;
-#pragma unroll
-  for (int i = 0; i < A::kLoads; ++i) {
-    const int q = A::load_of(i, wave);
-    int row, c;
-    A::chunk_of(q, row, c);
-    const int first = q * A::kRowsPerLoad;  // the load's rows are of one kind
-    const bool up = Cols::kGated && first % (2 * Cols::kWave) >= Cols::kWave;
-    const int col =
-        Cols::kGated ? row / (2 * Cols::kWave) * Cols::kWave + row % Cols::kWave : row;
-    a.off[i] = (uint32_t)min(col, cols - 1) * ld + (uint32_t)c * 16;
-    a.where[i] = (uint16_t)(c * 8);
-    ap[i] = w + (up ? (size_t)F * ld : 0);
-  }
 }
 
 // Bias, activation and residual on the accumulators, then the one rounding.
@@ -790,38 +372,8 @@ matmul_fp8_kernel(MatmulParams p, int ntiles) {
       lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
                 : p.weight_scales + ((size_t)t.e * (p.P / 128) + block + up) * kb;
   const char* bp = static_cast<const char*>(p.x) + (size_t)t.m0 * ld;
-  if (rows > C::kBv * 3 / 4)
-    prod.template run<C::kTv>(smem, wave, ap, bp, scale, kb, rows);
-  else if (rows > C::kBv / 2)
-    prod.template run<C::kTv * 3 / 4>(smem, wave, ap, bp, scale, kb, rows);
-  else if (rows > C::kBv / 4)
-    prod.template run<C::kTv / 2>(smem, wave, ap, bp, scale, kb, rows);
-  else
-    prod.template run<C::kTv / 4>(smem, wave, ap, bp, scale, kb, rows);
+  prod.run_rows(smem, wave, ap, bp, scale, kb, rows);
   finish<C, ACT>(prod, p, t, wave);
-}
-
-// The accumulators as bf16 rows: row v of the tile to out + v * ld, for v
-// below rows, columns below cols.  A whole tile takes kStores stores a lane.
-template <class C>
-constexpr int kStores = C::kTv * C::kTu / 2;
-
-template <class C, bool WHOLE, class Product>
-__device__ __forceinline__ void store_tile(const Product& prod, int wave, uint16_t* out, size_t ld,
-                                           int rows, int cols) {
-  const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
-#pragma unroll
-  for (int v = 0; v < C::kTv; ++v) {
-    const int m = (v * C::kWv + wv) * 16 + (lane & 15);
-    if (!WHOLE && m >= rows) continue;
-#pragma unroll
-    for (int a = 0; a < C::kTu / 2; ++a) {
-      const int c = (wu * C::kTu + 2 * a) * 16 + (lane >> 4) * 8;
-      float o[8];
-      prod.eight(o, a, v);
-      if (WHOLE || c < cols) store8(out + (size_t)m * ld + c, o);
-    }
-  }
 }
 
 // grad_x: D[input feature][token row].
@@ -933,19 +485,11 @@ using Large = Config<2, 2, 8, 8>;
 using Mid = Config<2, 2, 4, 4>;
 // 64 x 16 by four waves that share the steps.
 using Few = StreamProduct<4, 1, 4, 3>;
-// fp8, 256 token rows by 256 weight rows in two steps of LDS or by 128 in
+// fp8, 256 token rows by 256 weight rows in two steps of LDS (Codes) or by 128 in
 // three: the large tile moves less per product (32 experts of 4096 x 7168: 512
 // rows each 444 us against 527, 128 rows 236 against 284), the small one has
 // twice the blocks and the deeper ring for few rows (64 rows 201 against 195).
-using Codes = Config<2, 4, 8, 4>;
 using FewCodes = Config<2, 4, 4, 4>;
-
-constexpr int kUnits = 256;  // compute units
-
-int64_t tiles_of(const Segments& s, int u, int bu, int bv) {
-  const int64_t rows = s.pairs / s.E, busy = s.E < s.pairs ? s.E : s.pairs;
-  return busy * ((rows + bv - 1) / bv) * ((u + bu - 1) / bu);
-}
 
 // Large tiles from 112 rows an expert on, where some experts begin to need two
 // small ones (32 experts, 4096 x 7168: 96 rows 394 us against 357 on small
@@ -955,12 +499,6 @@ int64_t tiles_of(const Segments& s, int u, int bu, int bv) {
 // tiles 63 against 66).
 bool large_tiles(const Segments& s, int u) {
   return s.pairs / s.E >= 112 && tiles_of(s, u, Large::kBu, Large::kBv) >= kUnits * 3 / 4;
-}
-
-// The large fp8 tile where an expert has more than a quarter of its rows on
-// average and every compute unit gets one.
-bool large_codes(const Segments& s, int u) {
-  return s.pairs / s.E > Codes::kBv / 4 && tiles_of(s, u, Codes::kBu, Codes::kBv) >= kUnits;
 }
 
 // The streaming product for up to 4 rows an expert and 128 in all (one token of
@@ -986,24 +524,6 @@ bool large_weight_tiles(const Segments& s, int K, int P) {
   const int64_t tiles = (int64_t)s.E * ((K + Large::kBu - 1) / Large::kBu) *
                         ((P + Large::kBv - 1) / Large::kBv);
   return s.pairs / s.E > 64 && tiles >= kUnits * 3 / 4;
-}
-
-// A launch has less than 2^32 threads.
-bool launchable(int64_t blocks, int threads) { return blocks < (int64_t(1) << 32) / threads; }
-
-// More than 64 KB of LDS has to be asked for, once per kernel and device.
-template <auto KERNEL, int BYTES>
-hipError_t allow_lds() {
-  static std::atomic<uint64_t> done{0};
-  int device;
-  hipError_t e = hipGetDevice(&device);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = 1ull << (device & 63);
-  if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
-  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 template <class C, int ACT>

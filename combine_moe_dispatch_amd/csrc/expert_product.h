@@ -1,0 +1,603 @@
+// expert_product.h -- the tiled matrix products of the experts' rows: a block
+// holds a tile of D[u][v] = sum over r of A[u][r] B[v][r] in registers, in bf16
+// or in e4m3 with block scales, and what their kernels and launches share.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "expert_tile.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------------------
+// The tile product
+// ---------------------------------------------------------------------------
+// WU x WV waves of TU x TV fragments of 16 x 16.  A wave's fragments lie side
+// by side along u and kWv apart along v, so that the rows of a part tile are
+// spread over all waves.
+template <int WU, int WV, int TU, int TV>
+struct Config {
+  static constexpr int kWu = WU, kWv = WV, kTu = TU, kTv = TV;
+  static constexpr int kWaves = WU * WV, kThreads = kWaves * kWave;
+  static constexpr int kBu = WU * TU * 16, kBv = WV * TV * 16;
+};
+
+//
+// Four waves: with one wave to a SIMD each holds 128 x 128 of a 256 x 256 tile
+// and reads a quarter less from LDS per product than eight waves of 128 x 64
+// (prefill of 4096 tokens 1.62 against 1.73 ms; in two teams of four that
+// read and multiply in turns 1.80 ms, with 32 x 32 x 16 products 1.84 ms).
+// The matrix units draw the chip's power, so what counts is less work around
+// them rather than fewer idle cycles: the clock falls as those go.
+template <class C, bool AT, bool BT>
+struct TileProduct {
+  using A = OperandTile<C::kBu, C::kWaves, AT, true>;
+  using B = OperandTile<C::kBv, C::kWaves, BT, false>;
+  static constexpr int kStage = A::kBytes + B::kBytes;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLoads = A::kLoads + B::kLoads;
+  struct Fragments {
+    bf16x8_t a[C::kTu], b[C::kTv];
+  };
+  A a;
+  B b;
+  f32x4_t acc[C::kTu][C::kTv];
+  typename A::template Reader<C::kTu> ra;
+  typename B::template Reader<C::kTv> rb;
+
+  // A tile whose last quarters have no rows (only where B's rows run along r)
+  // leaves out their products and B's loads of them: PART is how many of the
+  // fragments along v a wave has to do, in quarters of kTv.
+  template <int PART>
+  static constexpr int kPartLoads = A::kLoads + B::kLoads * PART / C::kTv;
+
+  // Fragment i (of PART + kTu) of part k of the step at lds.
+  template <int PART, bool TAIL>
+  __device__ __forceinline__ void read(Fragments& f, int i, uint32_t lds, int k, int left) const {
+    if (i < PART)
+      f.b[i] = rb.template frag<TAIL>(lds + A::kBytes, i * (BT ? 1 : C::kWv), k, left);
+    else
+      f.a[i - PART] = ra.template frag<TAIL>(lds, i - PART, k, left);
+  }
+  template <int PART, bool TAIL>
+  __device__ __forceinline__ void read_all(Fragments& f, uint32_t lds, int k, int left) const {
+#pragma unroll
+    for (int i = 0; i < PART + C::kTu; ++i) read<PART, TAIL>(f, i, lds, k, left);
+  }
+
+  // acc += f, row of fragments by row, with before(u) in front of row u: what
+  // it issues runs beside the products.
+  template <int PART, class Before>
+  __device__ __forceinline__ void multiply(const Fragments& f, Before before) {
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u) {
+      before(u);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int v = 0; v < PART; ++v) mfma_in_place(acc[u][v], f.a[u], f.b[v]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
+  }
+
+  // A tile's operands: ap[i] is where load i of this wave starts in A (weight
+  // rows of a gated layer lie in two places), bp in B; lda, ldb are the
+  // operands' row pitches in bytes, red > 0 the positions along r.
+  const char* ap[A::kLoads];
+  const char* bp;
+  uint32_t lda, ldb;
+  int red, wave;
+  uint32_t lds;
+
+  __device__ __forceinline__ void setup(char* smem, int wave_) {
+    wave = wave_;
+    lds = lds_address(smem);
+    ra.init(wave % C::kWu * C::kTu * 16);
+    rb.init(wave / C::kWu * 16, C::kWv);
+  }
+  __device__ __forceinline__ int steps() const { return (red + kStep - 1) / kStep; }
+  // The next step's load i, and all of them.
+  template <bool TAIL>
+  __device__ __forceinline__ void load(int i, uint32_t to) {
+    const int rest = red % kStep;
+    if (i < A::kLoads)
+      a.template load<TAIL>(i, to, wave, ap[i], lda, rest);
+    else if (i < kLoads)
+      b.template load<TAIL>(i - A::kLoads, to + A::kBytes, wave, bp, ldb, rest);
+  }
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int i = 0; i < A::kLoads; ++i) ap[i] += AT ? (size_t)kStep * lda : (size_t)kStep * 2;
+    bp += BT ? (size_t)kStep * ldb : (size_t)kStep * 2;
+  }
+  template <int PART>
+  __device__ __forceinline__ void start(uint32_t to, bool full) {
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < kPartLoads<PART>; ++i) load<false>(i, to);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPartLoads<PART>; ++i) load<true>(i, to);
+    }
+    advance();
+  }
+  // Start the first two steps of a tile.  No wave may still read LDS.
+  template <int PART>
+  __device__ __forceinline__ void begin() {
+    const int whole = red / kStep;
+    start<PART>(lds, whole > 0);
+    if (steps() > 1) start<PART>(lds + kStage, whole > 1);
+  }
+
+  // The tile that begin() has started.  Afterwards LDS is free again.  behind:
+  // stores that this wave has started since (0, or kStores at least).
+  template <int PART>
+  __device__ __forceinline__ void run(int behind) {
+    constexpr int kLoads = kPartLoads<PART>;
+    constexpr int kBehind = C::kTv * C::kTu / 2;
+    static_assert(kLoads + kBehind < 64, "counted by the hardware");
+    static_assert(kParts == 2, "the parts are written out");
+    clear();
+    uint32_t here = lds, next = lds + kStage;
+    const int steps = this->steps(), whole = red / kStep;
+    const int rest = red - (steps - 1) * kStep;  // positions of the last step
+    // Every wave's reads of `here` are in registers and its loads of `next` in
+    // LDS: `here` may be filled again and `next` be read.
+    auto meet = [&] {
+      wait_lds();
+      wait_vm<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    auto turn = [&] {
+      const uint32_t h = here;
+      here = next;
+      next = h;
+    };
+    constexpr int kReads = (2 * (C::kTu + PART) + C::kTu - 1) / C::kTu;  // in the first rows
+    constexpr int kStarts = (kLoads + C::kTu - 1) / C::kTu;
+    auto reading = [&](Fragments& f, uint32_t lds, int k, int u) {
+#pragma unroll
+      for (int i = u * kReads; i < (u + 1) * kReads; ++i)
+        if (i < C::kTu + PART) read<PART, false>(f, i, lds, k, rest);
+    };
+    const auto nothing = [](int) {};
+    Fragments f0, f1;
+    if (steps > 1 && behind > 0)
+      wait_vm<kLoads + kBehind>();
+    else if (steps > 1)
+      wait_vm<kLoads>();
+    else
+      wait_vm<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (steps > 1)
+      read_all<PART, false>(f0, here, 0, rest);
+    else
+      read_all<PART, true>(f0, here, 0, rest);
+    // Half a step is multiplied while the next half is read, the second half
+    // behind the barrier, so that the matrix units have work on both sides.
+    for (int t = 0; t + 2 < whole; ++t) {
+      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
+      meet();
+      multiply<PART>(f1, [&](int u) {
+        reading(f0, next, 0, u);
+#pragma unroll
+        for (int i = u * kStarts; i < (u + 1) * kStarts; ++i)
+          if (i < kLoads) load<false>(i, here);
+      });
+      advance();
+      turn();
+    }
+    if (whole < steps && steps > 2) {  // the step whose loads are the short ones
+      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
+      meet();
+      start<PART>(here, false);
+      multiply<PART>(f1, [&](int u) { reading(f0, next, 0, u); });
+      turn();
+    }
+    if (steps > 1) {
+      multiply<PART>(f0, [&](int u) { reading(f1, here, 1, u); });
+      meet();
+      multiply<PART>(f1, nothing);
+      read_all<PART, true>(f0, next, 0, rest);
+      turn();
+    }
+    // the second half of the last step may have no positions (a weight gradient
+    // over 256 rows an expert 3% less)
+    if (rest > kPart) read_all<PART, true>(f1, here, 1, rest);
+    multiply<PART>(f0, nothing);
+    wait_lds();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (rest > kPart) multiply<PART>(f1, nothing);
+    mfma_results();
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) mfma_result(acc[u][v]);
+  }
+
+  // A tile of `rows` along v, from its first load on.
+  template <int PART>
+  __device__ __forceinline__ void begin_and_run() {
+    static_assert(!BT, "the front of a transposed operand's tile is not its first columns");
+    begin<PART>();
+    run<PART>(0);
+  }
+  __device__ __forceinline__ void begin_and_run(int rows) {
+    if (rows > C::kBv * 3 / 4)
+      begin_and_run<C::kTv>();
+    else if (rows > C::kBv / 2)
+      begin_and_run<C::kTv * 3 / 4>();
+    else if (rows > C::kBv / 4)
+      begin_and_run<C::kTv / 2>();
+    else
+      begin_and_run<C::kTv / 4>();
+  }
+
+  // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours
+  // along u from a * 32 + (lane >> 4) * 8 on, of the fragment's row lane & 15.
+  __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
+  }
+};
+
+// ---------------------------------------------------------------------------
+// An e4m3 operand held transposed: one step is 128 rows along r of SIZE columns,
+// [128][SIZE] bytes in LDS, read back through the transposing 8-byte load: of 16
+// lanes, lane j names 8 bytes of row j / 2 (columns 0-7 or 8-15) and receives
+// column j of the 8 rows.  As in OperandTile the layout is linear in the lanes and
+// chunk c of row i sits in slot c ^ f(i): the 16 rows that half a wave reads from
+// (two runs of 8, 16 apart) take 16 different places of the 256 bytes of banks.
+// A lane receives its 32 positions in the order of the other operand's chunks,
+// 16 (l >> 4) .. + 15 and 64 behind.
+// ---------------------------------------------------------------------------
+template <int SIZE, int WAVES>
+struct TransposedCodes {
+  static constexpr int kBytes = SIZE * 128;
+  static constexpr int kLoads = kBytes / 1024 / WAVES;
+  static_assert(kLoads * WAVES * 1024 == kBytes, "whole wave loads");
+  static_assert(SIZE == 256, "the swizzle is that of rows of 256 bytes");
+  static constexpr int kSlots = SIZE / 16;
+  static constexpr int kRowsPerLoad = 64 / kSlots;
+  uint32_t off[kLoads];
+
+  static __device__ __forceinline__ int swizzle(int row) {
+    return (row & 7) | ((row >> 4) & 1) << 3;
+  }
+  static __device__ __forceinline__ int load_of(int i, int wave) { return i * WAVES + wave; }
+  // ld: bytes between rows.  valid: columns the tile really has (a multiple of
+  // 16); past them the last ones are read again.
+  __device__ __forceinline__ void init(int wave, uint32_t ld, int valid) {
+    const int lane = lane_id();
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = load_of(i, wave) * kRowsPerLoad + lane / kSlots;
+      const int c = (lane % kSlots) ^ swizzle(row);
+      off[i] = (uint32_t)row * ld + (uint32_t)min(c * 16, valid - 16);
+    }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void load(int i, uint32_t lds, int wave, const char* base, uint32_t,
+                                       int) const {
+    load_to_lds(lds + (uint32_t)load_of(i, wave) * 1024, base, off[i]);
+  }
+
+  template <int N>
+  struct Reader {
+    static constexpr bool kWhole = true;  // a fragment comes as one
+    uint32_t at[N];
+    __device__ __forceinline__ void init(int i0) {
+      const int lane = lane_id(), j = lane & 15, row = (lane >> 4) * 16 + (j >> 1);
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        at[n] = (uint32_t)(row * SIZE + ((i0 / 16 + n) ^ swizzle(row)) * 16 + (j & 1) * 8);
+    }
+    __device__ __forceinline__ i32x8_t frag(uint32_t lds, int n) const {
+      union {
+        i32x2_t q[4];
+        i32x8_t v;
+      } u;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        u.q[q] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i32x2_t*)(uintptr_t)(
+                lds + at[n] + (q / 2 * 64 + q % 2 * 8) * SIZE));
+      return u.v;
+    }
+  };
+};
+
+// ---------------------------------------------------------------------------
+// The same for e4m3 operands with a scale per 128 values along r: one step is
+// one block of 128, whose products are summed by one 16 x 16 x 128 matrix
+// instruction per fragment and then scaled in fp32, sx of the token times sw
+// of the 128 weight rows.  A row of a step is 128 bytes, as in the bf16
+// product, so the tiles in LDS are the same; the chunks of a fragment are
+// taken in an order of their own, equal for both operands, which a sum does
+// not notice.  Eight waves, two on every SIMD: one scales while the other
+// multiplies.
+//
+// The instruction's own sum has fewer bits than fp32: of 8 neighbouring columns
+// it cuts every product below 2^-13 of the largest (measured; the 16 x 16 x 32
+// instruction does the same), so a sum is off by less than 2^-10 of the groups'
+// largest products (2.5 2^-13 at most in 10^5 sums of random codes, 2^-19 of the
+// magnitudes in the mean of normal ones).  Both factors of a product were
+// rounded to 2^-4 before, and exact sums would need the codes widened to bf16, at
+// half the rate.
+//
+// AT: A is held transposed, its rows along r.  Its fragments are not paired, so
+// that a lane's eight neighbours come from an exchange between the lanes behind
+// the last product.
+// ---------------------------------------------------------------------------
+template <class C, int STAGES, bool AT = false>
+struct Fp8Product {
+  using A = std::conditional_t<AT, TransposedCodes<C::kBu, C::kWaves>,
+                               OperandTile<C::kBu, C::kWaves, false, true>>;
+  using B = OperandTile<C::kBv, C::kWaves, false, false>;
+  static constexpr int kScales = C::kWaves * 256;  // one dword a lane
+  static_assert(C::kBv <= C::kWaves * 32, "a wave brings in the scales of 32 rows");
+  static constexpr int kStage = A::kBytes + B::kBytes + kScales;
+  static constexpr int kLds = STAGES * kStage;
+  static constexpr int kRows = 4;  // of fragments multiplied at a time
+  A a;
+  B b;
+  f32x4_t acc[C::kTu][C::kTv];
+  typename A::template Reader<C::kTu> ra;
+  typename B::template Reader<C::kTv> rb;
+
+  size_t a_step;   // AT: bytes between the steps of A,
+  int scale_step;  // and entries between this lane's scales
+
+  template <class R>
+  static __device__ __forceinline__ i32x8_t frag(const R& r, uint32_t lds, int n) {
+    if constexpr (R::kWhole) {
+      return r.frag(lds, n);
+    } else {
+      union {
+        bf16x8_t h[2];
+        i32x8_t v;
+      } u;
+      u.h[0] = r.template frag<false>(lds, n, 0, 0);
+      u.h[1] = r.template frag<false>(lds, n, 1, 0);
+      return u.v;
+    }
+  }
+
+  // PART: as in TileProduct.  blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
+  // 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of the weight rows
+  // behind the first and the second half of the wave's fragments.  (A plain
+  // load of them would wait for every load to LDS before it.)  rows: how many
+  // the tile has.
+  template <int PART>
+  __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
+                                      const char* bp, const float* scale, int blocks, int rows) {
+    constexpr int kRowLoads = B::kLoads * PART / C::kTv;
+    constexpr int kLoads = A::kLoads + kRowLoads + 1;
+    ra.init(wave % C::kWu * C::kTu * 16);
+    rb.init(wave / C::kWu * 16);
+#pragma unroll
+    for (int u = 0; u < C::kTu; ++u)
+#pragma unroll
+      for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
+    const uint32_t lds = lds_address(smem), lds_end = lds + kLds;
+    uint32_t fill = lds, here = lds;
+    auto after = [&](uint32_t slot) { return slot + kStage == lds_end ? lds : slot + kStage; };
+    auto start = [&] {
+#pragma unroll
+      for (int i = 0; i < A::kLoads; ++i) {
+        a.template load<false>(i, fill, wave, ap[i], 0, 0);
+        ap[i] += AT ? a_step : 128;
+      }
+#pragma unroll
+      for (int i = 0; i < kRowLoads; ++i)
+        b.template load<false>(i, fill + A::kBytes, wave, bp, 0, 0);
+      load4_to_lds(fill + A::kBytes + B::kBytes + wave * 256, scale);
+      bp += 128;
+      scale += AT ? scale_step : 1;
+      fill = after(fill);
+    };
+    for (int t = 0; t < STAGES - 1 && t < blocks; ++t) start();
+    // the fragments of this wave that hold rows at all
+    const int wv = wave / C::kWu;
+    const int nv = min((rows - wv * 16 + C::kWv * 16 - 1) / (C::kWv * 16), C::kTv);
+    // 32 rows of scales every 256 bytes, this wave's two behind its own 32
+    const uint32_t scales = A::kBytes + B::kBytes;
+    const uint32_t sw_at = scales + wave * 256 + 128;
+    const uint32_t sx_at = scales + wv / 2 * 256 + wv % 2 * 64 + (lane_id() & 15) * 4;
+    static_assert(C::kWv % 2 == 0, "a fragment's scales lie 256 bytes per two fragments on");
+    auto lds_float = [](uint32_t p) {
+      return *(const __attribute__((address_space(3))) float*)(uintptr_t)p;
+    };
+    for (int t = 0; t < blocks; ++t) {
+      if (t + STAGES - 1 <= blocks)
+        wait_vm<(STAGES - 2) * kLoads>();
+      else
+        wait_vm<0>();
+      wait_lds();  // this wave has read the step before out
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (t + STAGES - 1 < blocks) start();
+      if (nv > 0) {
+        const float sw[2] = {lds_float(here + sw_at), lds_float(here + sw_at + 4)};
+#pragma unroll
+        for (int u0 = 0; u0 < C::kTu; u0 += kRows) {
+          i32x8_t fa[kRows];
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) fa[u] = frag(ra, here, u0 + u);
+#pragma unroll
+          for (int v = 0; v < PART; ++v) {
+            if (v >= nv) break;
+            const i32x8_t fb = frag(rb, here + A::kBytes, v * C::kWv);
+            const float sx = lds_float(here + sx_at + v * C::kWv / 2 * 256);
+            f32x4_t part[kRows];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+              part[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[u], fb, f32x4_t{}, 0,
+                                                                         0, 0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+              const float s = sx * sw[u0 + u < C::kTu / 2 ? 0 : 1];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[u0 + u][v][i] = fmaf(part[u][i], s, acc[u0 + u][v][i]);
+            }
+          }
+        }
+      }
+      here = after(here);
+    }
+  }
+
+  // A tile of `rows` rows: as many quarters (halves) of it as have some.
+  __device__ __forceinline__ void run_rows(char* smem, int wave, const char* (&ap)[A::kLoads],
+                                           const char* bp, const float* scale, int blocks,
+                                           int rows) {
+    if constexpr (C::kTv % 4 == 0) {
+      if (rows > C::kBv * 3 / 4)
+        run<C::kTv>(smem, wave, ap, bp, scale, blocks, rows);
+      else if (rows > C::kBv / 2)
+        run<C::kTv * 3 / 4>(smem, wave, ap, bp, scale, blocks, rows);
+      else if (rows > C::kBv / 4)
+        run<C::kTv / 2>(smem, wave, ap, bp, scale, blocks, rows);
+      else
+        run<C::kTv / 4>(smem, wave, ap, bp, scale, blocks, rows);
+    } else {
+      static_assert(C::kTv % 2 == 0 && B::kLoads % 2 == 0, "whole loads of half a tile");
+      if (rows > C::kBv / 2)
+        run<C::kTv>(smem, wave, ap, bp, scale, blocks, rows);
+      else
+        run<C::kTv / 2>(smem, wave, ap, bp, scale, blocks, rows);
+    }
+  }
+
+  // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours along
+  // u, from column(a) of the wave's on.
+  __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
+    if constexpr (AT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // lanes 16-31 and 48-63 of the first for 0-15 and 32-47 of the second
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[2 * a][v][i]),
+                                                        __float_as_uint(acc[2 * a + 1][v][i]),
+                                                        false, false);
+        o[i] = __uint_as_float(r[0]);
+        o[4 + i] = __uint_as_float(r[1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
+    }
+  }
+  static __device__ __forceinline__ int column(int a) {
+    const int g = lane_id() >> 4;
+    return a * 32 + (AT ? (g & 1) * 16 + (g >> 1) * 8 : g * 8);
+  }
+};
+
+__device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+// y (and pre): u runs over weight rows; a gated layer's wave takes half of its
+// fragments from the gate rows and half from the up rows of the same columns.
+template <class C, int ACT>
+struct Columns {
+  static constexpr bool kGated = ACT == kActSwiglu;
+  static constexpr int kPairs = (kGated ? C::kTu / 2 : C::kTu) / 2;  // along the output's columns
+  static constexpr int kWave = kPairs * 32;                          // output columns of a wave
+  static constexpr int kTile = kWave * C::kWu;                       // and of the tile
+};
+
+// This wave's loads of weight rows: w is the first of the tile's (gate) rows,
+// cols how many columns are left from there, ld the bytes of a row.
+template <class C, int ACT, class A>
+__device__ __forceinline__ void weight_loads(A& a, const char* (&ap)[A::kLoads], const char* w,
+                                             int wave, int F, int cols, uint32_t ld) {
+  using Cols = Columns<C, ACT>;
+#pragma unroll
+  for (int i = 0; i < A::kLoads; ++i) {
+    const int q = A::load_of(i, wave);
+    int row, c;
+    A::chunk_of(q, row, c);
+    const int first = q * A::kRowsPerLoad;  // the load's rows are of one kind
+    const bool up = Cols::kGated && first % (2 * Cols::kWave) >= Cols::kWave;
+    const int col =
+        Cols::kGated ? row / (2 * Cols::kWave) * Cols::kWave + row % Cols::kWave : row;
+    a.off[i] = (uint32_t)min(col, cols - 1) * ld + (uint32_t)c * 16;
+    a.where[i] = (uint16_t)(c * 8);
+    ap[i] = w + (up ? (size_t)F * ld : 0);
+  }
+}
+
+// The accumulators as bf16 rows: row v of the tile to out + v * ld, for v
+// below rows, columns below cols.  A whole tile takes kStores stores a lane.
+template <class C>
+constexpr int kStores = C::kTv * C::kTu / 2;
+
+template <class C, bool WHOLE, class Product>
+__device__ __forceinline__ void store_tile(const Product& prod, int wave, uint16_t* out, size_t ld,
+                                           int rows, int cols) {
+  const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int m = (v * C::kWv + wv) * 16 + (lane & 15);
+    if (!WHOLE && m >= rows) continue;
+#pragma unroll
+    for (int a = 0; a < C::kTu / 2; ++a) {
+      const int c = (wu * C::kTu + 2 * a) * 16 + (lane >> 4) * 8;
+      float o[8];
+      prod.eight(o, a, v);
+      if (WHOLE || c < cols) store8(out + (size_t)m * ld + c, o);
+    }
+  }
+}
+
+constexpr int kUnits = 256;  // compute units
+
+inline int64_t tiles_of(const Segments& s, int u, int bu, int bv) {
+  const int64_t rows = s.pairs / s.E, busy = s.E < s.pairs ? s.E : s.pairs;
+  return busy * ((rows + bv - 1) / bv) * ((u + bu - 1) / bu);
+}
+
+using Codes = Config<2, 4, 8, 4>;
+// The large fp8 tile where an expert has more than a quarter of its rows on
+// average and every compute unit gets one.
+inline bool large_codes(const Segments& s, int u) {
+  return s.pairs / s.E > Codes::kBv / 4 && tiles_of(s, u, Codes::kBu, Codes::kBv) >= kUnits;
+}
+
+// A launch has less than 2^32 threads.
+inline bool launchable(int64_t blocks, int threads) { return blocks < (int64_t(1) << 32) / threads; }
+
+// More than 64 KB of LDS has to be asked for, once per kernel and device.
+template <auto KERNEL, int BYTES>
+hipError_t allow_lds() {
+  static std::atomic<uint64_t> done{0};
+  int device;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (device & 63);
+  if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+}  // namespace moe

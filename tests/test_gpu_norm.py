@@ -1,0 +1,317 @@
+"""The RMS norm, its gradient and 8-bit weights against plain fp64 forms: one row to
+many, every thread layout, odd sizes, optional outputs, in-place use, masks of NaN
+and infinities, empty rows and blocks."""
+import numpy as np
+import pytest
+import torch
+
+import ffn_reference as plain
+from combine_moe_dispatch_amd import api
+from expert_reference import TINY, U16
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+FILL = -7.0
+
+
+def rows(T, H, seed, loud=True):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, generator=gen)
+    if loud:
+        x = x * (1 + 20.0 * (torch.rand(H, generator=gen) < 0.01))
+    return x.bfloat16()
+
+
+def norm_weight(H, seed):
+    return 1.0 + 0.2 * torch.randn(H, generator=torch.Generator().manual_seed(seed + 100))
+
+
+def out(T, H, dtype=torch.bfloat16):
+    fill = 0x55 if dtype == torch.uint8 else FILL
+    return torch.full((T + 1, H), fill, dtype=dtype, device="cuda")  # one canary row
+
+
+def check(got, want, bound, what):
+    off = (got.double().cpu() - want).abs()
+    assert (off <= bound).all(), (what, float((off - bound).max()))
+
+
+def check_codes(codes, scales, v, dv):
+    """Codes within the two that the value's error allows, scales within theirs."""
+    got = codes.cpu().view(torch.float8_e4m3fn).double()
+    value, slack = plain.quantize(v, dv)
+    s = scales.double().cpu()
+    check((got.unflatten(1, (-1, 128)) * s[..., None]).flatten(1), value, slack + TINY, "8-bit rows")
+    want = v.abs().unflatten(1, (-1, 128)).amax(2) / 448
+    ds = dv.unflatten(1, (-1, 128)).amax(2) / 448
+    check(s, want, ds + 2.0 ** -23 * want + TINY, "scales")
+
+
+def run(T, H, residual=True, codes=True, y=True, total=True, inv=True, seed=0):
+    x, w = rows(T, H, seed), norm_weight(H, seed)
+    res = rows(T, H, seed + 1, loud=False) if residual else None
+    t, yy, inv_ = (out(T, H) if total else None), (out(T, H) if y else None), None
+    c, s = (out(T, H, torch.uint8), out(T, H // 128, torch.float32)) if codes else (None, None)
+    if inv:
+        inv_ = torch.full((T + 1,), FILL, device="cuda")
+    api.moe_rms_norm(x.cuda(), None if res is None else res.cuda(), w.cuda(), EPS, t, yy, c, s, inv_)
+    want_t = x if res is None else (x.float() + res.float()).bfloat16()
+    v, dv, r, dr = plain.norm(want_t.double(), w.double(), EPS)
+    if total:
+        assert torch.equal(t[:T].cpu(), want_t) and (t[T] == FILL).all()
+    if y:
+        check(yy[:T], v, plain.rounded16(v, dv), "y")
+        assert (yy[T] == FILL).all()
+    if codes:
+        check_codes(c[:T], s[:T], v, dv)
+        assert (c[T] == 0x55).all() and (s[T] == FILL).all()
+    if inv:
+        check(inv_[:T], r, dr, "1 / rms")
+        assert inv_[T] == FILL
+
+
+@pytest.mark.parametrize("T,H", [(1, 128), (1, 7168), (2, 8192), (3, 8320), (255, 384), (256, 2048),
+                                 (257, 2176), (300, 4096), (257, 4224), (700, 128), (1500, 256),
+                                 (270, 8192), (5, 16384), (3, 16512), (2, 32768), (2, 40960),
+                                 (1, 65536)])
+def test_norm(T, H):
+    run(T, H, seed=T + H)
+
+
+@pytest.mark.parametrize("T,H", [(1, 8), (7, 72), (300, 1432), (257, 2056), (4, 20008), (2100, 8)])
+def test_norm_of_odd_rows(T, H):
+    run(T, H, codes=False, seed=T)
+    run(T, H, codes=False, residual=False, seed=T)
+
+
+@pytest.mark.parametrize("kw", [dict(residual=False), dict(y=False), dict(codes=False),
+                                dict(total=False), dict(inv=False),
+                                dict(residual=False, total=False, y=False, inv=False),
+                                dict(total=False, y=False, codes=False)])
+def test_norm_with_some_outputs(kw):
+    run(40, 640, **kw)
+    run(400, 640, **kw)
+
+
+@pytest.mark.parametrize("T", [3, 2500])
+def test_norm_in_place(T):
+    """total over the residual and y over x; rows of several passes of a block."""
+    H = 512
+    x, res, w = rows(T, H, 5).cuda(), rows(T, H, 6).cuda(), norm_weight(H, 5).cuda()
+    t, y = torch.empty_like(x), torch.empty_like(x)
+    api.moe_rms_norm(x, res, w, EPS, t, y)
+    api.moe_rms_norm(x, res, w, EPS, res, x)
+    assert torch.equal(res, t) and torch.equal(x, y)
+
+
+def test_norm_of_special_rows():
+    """Zeros, a NaN, an infinity, the largest and the smallest values, a block of zeros."""
+    H = 384
+    x = rows(8, H, 9)
+    x[0] = 0
+    x[1, 5] = float("nan")
+    x[2, 130] = float("inf")
+    x[3] = 1e15
+    x[4] = 1e-30
+    x[5, 128:256] = 0
+    w = torch.ones(H)
+    w[256:] = 0                     # a block that the weights clear
+    xg = x.cuda()
+    y, c = torch.empty_like(xg), torch.empty(8, H, dtype=torch.uint8, device="cuda")
+    s = torch.empty(8, H // 128, device="cuda")
+    api.moe_rms_norm(xg, None, w.cuda(), EPS, None, y, c, s)
+    y, c, s = y.cpu(), c.cpu().view(torch.float8_e4m3fn).float(), s.cpu()
+    assert (y[0] == 0).all() and (c[0] == 0).all() and (s[0] == 0).all()
+    assert y[1].isnan().all() and s[1].isnan().all() and c[1].isnan().all()
+    assert y[2, 130].isnan() and s[2, 1].isnan() and c[2, 128:256].isnan().all()
+    fine = [3, 4, 5, 6, 7]
+    v, dv, _, _ = plain.norm(x[fine].double(), w.double(), EPS)
+    check(y[fine], v, plain.rounded16(v, dv), "y")
+    assert (c[fine][:, 256:] == 0).all() and (s[fine, 2] == 0).all() and (c[5, 128:256] == 0).all()
+    assert (c[3, :256] == 448).all()
+
+
+def test_codes_of_infinite_values():
+    """A norm cannot give infinities of its own; a weight can."""
+    H = 128
+    w = torch.ones(H)
+    w[3] = float("inf")
+    x = torch.ones(1, H, dtype=torch.bfloat16, device="cuda")
+    c, s = torch.empty(1, H, dtype=torch.uint8, device="cuda"), torch.empty(1, 1, device="cuda")
+    api.moe_rms_norm(x, None, w.cuda(), EPS, None, None, c, s)
+    c = c.cpu().view(torch.float8_e4m3fn).float()[0]
+    assert s.item() == float("inf") and c[3].isnan()
+    assert (c[torch.arange(H) != 3] == 0).all()
+
+
+def grads(T, H, carried=True, gx=True, gw=True, seed=0):
+    t, w = rows(T, H, seed), norm_weight(H, seed)
+    gen = torch.Generator().manual_seed(seed + 7)
+    gy = (0.01 * torch.randn(T, H, generator=gen)).bfloat16()
+    c = (0.01 * torch.randn(T, H, generator=gen)).bfloat16() if carried else None
+    r = (t.double().square().mean(1) + EPS).rsqrt().float()
+    x_out = out(T, H) if gx else None
+    w_out = torch.full((H + 8,), FILL, device="cuda") if gw else None
+    ws = api.alloc_rms_norm_workspace(T, H, "cuda")
+    if ws is not None:
+        ws.fill_(0xFF)
+    api.moe_rms_norm_backward(gy.cuda(), t.cuda(), w.cuda(), r.cuda(),
+                              None if c is None else c.cuda(), x_out, w_out, ws)
+    want_x, want_w = plain.norm_grad(gy.double(), t.double(), w.double(), r.double(),
+                                     None if c is None else c.double())
+    if gx:
+        check(x_out[:T], *want_x, "grad_x")
+        assert (x_out[T] == FILL).all()
+    if gw:
+        check(w_out[:H], *want_w, "grad_weight")
+        assert (w_out[H:] == FILL).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 8), (1, 7168), (2, 72), (9, 8200), (255, 1432), (256, 2048),
+                                 (257, 2056), (513, 264), (600, 4096), (300, 8192), (2100, 136),
+                                 (3, 16384), (5, 16392), (2, 40960), (1, 65536)])
+def test_norm_gradient(T, H):
+    grads(T, H, seed=T + H)
+
+
+@pytest.mark.parametrize("kw", [dict(carried=False), dict(gx=False), dict(gw=False)])
+def test_norm_gradient_of_some(kw):
+    grads(33, 640, **kw)
+    grads(900, 640, **kw)
+
+
+def test_norm_gradient_without_rows():
+    w = torch.ones(64, device="cuda")
+    gw = torch.full((64,), FILL, device="cuda")
+    none = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    api.moe_rms_norm_backward(none, none, w, w[:0], None, none, gw)
+    assert (gw == 0).all()
+
+
+def test_norm_gradient_in_place_and_repeatable():
+    T, H = 1500, 1024
+    t, w = rows(T, H, 3).cuda(), norm_weight(H, 3).cuda()
+    gy, c = rows(T, H, 4).cuda(), rows(T, H, 5).cuda()
+    r = (t.double().square().mean(1) + EPS).rsqrt().float()
+    gx, gw = torch.empty_like(t), torch.empty(H, device="cuda")
+    api.moe_rms_norm_backward(gy, t, w, r, c, gx, gw)
+    for over in (gy.clone(), c.clone()):
+        again = torch.empty_like(gw)
+        same = over.equal(gy)
+        api.moe_rms_norm_backward(over if same else gy, t, w, r, c if same else over, over, again)
+        assert torch.equal(over, gx) and torch.equal(again, gw)
+
+
+def test_norm_gradient_against_differences():
+    """The library's own forward sums, read through a linear loss: its rows are
+    rounded to bf16, so the steps are wide and the tolerance counts those roundings."""
+    T, H = 4, 64
+    gen = torch.Generator().manual_seed(2)
+    t = torch.randn(T, H, generator=gen).bfloat16()
+    gy = torch.randn(T, H, generator=gen).bfloat16()
+    w = norm_weight(H, 2)
+    r = torch.empty(T, device="cuda")
+    api.moe_rms_norm(t.cuda(), None, w.cuda(), EPS, None, None, None, None, r)
+    gx = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    api.moe_rms_norm_backward(gy.cuda(), t.cuda(), w.cuda(), r, None, gx, None)
+    d = torch.randn(T, H, generator=gen)
+    d = d / d.norm(dim=1, keepdim=True)
+    step = 0.5  # a change of 2^-4 of a row: the third difference is some 2^-8 of the first
+
+    def loss(x):
+        y = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+        api.moe_rms_norm(x.cuda(), None, w.cuda(), EPS, None, y)
+        return (y.double().cpu() * gy.double()).sum(1)
+
+    hi, lo = (t.float() + step * d).bfloat16(), (t.float() - step * d).bfloat16()
+    got = loss(hi) - loss(lo)
+    want = (gx.double().cpu() * (hi.double() - lo.double())).sum(1)
+    # both losses round each of H values to half a bf16 step; gx as well; and the
+    # cubic term, |d|^2 / H of the first (rms is 1 here)
+    v = plain.norm(t.double(), w.double(), EPS)[0].abs()
+    bound = 2 * U16 * (1.5 * v * gy.double().abs()).sum(1) + \
+        U16 * (gx.double().cpu() * (hi.double() - lo.double())).abs().sum(1) + \
+        step ** 2 / H * 4 * gy.double().norm(dim=1) * 2 * step
+    assert ((got - want).abs() <= bound).all()
+    assert (want.abs() > bound).any()   # the check says something
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,P,K", [(1, 128, 128), (3, 384, 128), (2, 128, 640), (5, 256, 1280)])
+def test_weights(E, P, K, dtype):
+    """Bit for bit the definition's fp32 divisions."""
+    gen = torch.Generator().manual_seed(P + K)
+    w = torch.randn(E, P, K, generator=gen)
+    w[0, :128, :128] = 0
+    w[-1, -1, -1] = 77.0                         # one outlier rules its block
+    w[-1, -128:, :128] *= 1e-37                  # a scale below the ordinary range
+    w[E // 2, :128, -128:] *= 1e30
+    w = w.to(dtype)
+    codes = torch.full((E * P * K + 8,), 0x55, dtype=torch.uint8, device="cuda")
+    scales = torch.full((E * P * K // 16384 + 1,), FILL, device="cuda")
+    api.moe_quantize_weight(w.cuda(), codes, scales)
+    b = w.float().numpy().reshape(E, P // 128, 128, K // 128, 128)
+    s = np.abs(b).max((2, 4)) / np.float32(448)
+    with np.errstate(all="ignore"):
+        q = np.where(s[:, :, None, :, None] > 0, b / s[:, :, None, :, None], np.float32(0))
+    want = plain.e4m3(torch.from_numpy(q.astype(np.float64))).view(E, P, K)
+    assert np.array_equal(scales[:-1].cpu().numpy().reshape(s.shape), s) and scales[-1] == FILL
+    got = codes[:-8].cpu().view(torch.float8_e4m3fn).double().view(E, P, K)
+    assert torch.equal(got, want)
+    assert (codes[-8:] == 0x55).all()
+
+
+def test_weights_with_a_nan():
+    w = torch.ones(128, 256)
+    w[7, 200] = float("nan")
+    w[9, 3] = float("-inf")
+    codes, scales = torch.empty(128, 256, dtype=torch.uint8, device="cuda"), torch.empty(2, device="cuda")
+    api.moe_quantize_weight(w.cuda(), codes, scales)
+    got = codes.cpu().view(torch.float8_e4m3fn).float()
+    assert scales[1].isnan() and got[:, 128:].isnan().all()
+    assert scales[0] == float("inf") and got[9, 3].isnan()
+    got[9, 3] = 0
+    assert (got[:, :128] == 0).all()
+
+
+def test_refusals_on_tensors():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(256, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        api.moe_rms_norm(x.t().contiguous().t(), None, w, EPS, None, x)
+    with pytest.raises(ValueError, match="weight holds"):
+        api.moe_rms_norm(x, None, w[:8], EPS, None, x)
+    with pytest.raises(TypeError, match="weight must be"):
+        api.moe_rms_norm(x, None, w.bfloat16(), EPS, None, x)
+    with pytest.raises(ValueError, match="scales holds"):
+        api.moe_rms_norm(x, None, w, EPS, None, None, x.view(torch.uint8), w[:1])
+    with pytest.raises(api.MoeError, match="INVALID"):
+        api.moe_rms_norm(x, None, w, EPS, x, x)
+    with pytest.raises(TypeError, match="weight must be"):
+        api.moe_quantize_weight(x.half(), x.view(torch.uint8), w)
+    with pytest.raises(api.MoeError):                    # 4 rows are no block
+        api.moe_quantize_weight(x, x.view(torch.uint8), w)
+
+
+def test_rows_past_2_31_elements():
+    """Offsets that pass 32 bits."""
+    T, H = 300001, 7168
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(0)
+    at = [0, 149797, 149798, 299593, 300000]
+    x[at] = torch.randn(5, H, generator=gen).bfloat16().cuda()
+    w = norm_weight(H, 0)
+    y, c = torch.empty_like(x), torch.empty(T, H, dtype=torch.uint8, device="cuda")
+    s = torch.empty(T, H // 128, device="cuda")
+    inv = torch.empty(T, device="cuda")
+    api.moe_rms_norm(x, None, w.cuda(), EPS, None, y, c, s, inv)
+    v, dv, r, dr = plain.norm(x[at].double().cpu(), w.double(), EPS)
+    check(y[at], v, plain.rounded16(v, dv), "y")
+    check_codes(c[at], s[at], v, dv)
+    gx, gw = torch.empty_like(x), torch.empty(H, device="cuda")
+    api.moe_rms_norm_backward(x, x, w.cuda(), inv, None, gx, gw)
+    t = x[at].double().cpu()
+    want_x, want_w = plain.norm_grad(t, t, w.double(), inv[at].double().cpu(), None)
+    check(gx[at], *want_x, "grad_x")
+    check(gw, want_w[0], want_w[1], "grad_weight")   # the other rows are zeros
