@@ -285,6 +285,7 @@ __device__ __forceinline__ void transposed_product(Product& prod, char* smem, co
   prod.scale_step = lane < 32 ? 1 : cb;
   prod.run_rows(smem, wave, ap, reinterpret_cast<const char*>(rows_codes) + (size_t)t.m0 * red,
                 scale, rb, rows);
+  prod.exchange();
 }
 
 template <class C>

@@ -348,7 +348,6 @@ struct Fp8Product {
   static_assert(C::kBv <= C::kWaves * 32, "a wave brings in the scales of 32 rows");
   static constexpr int kStage = A::kBytes + B::kBytes + kScales;
   static constexpr int kLds = STAGES * kStage;
-  static constexpr int kRows = 4;  // of fragments multiplied at a time
   A a;
   B b;
   f32x4_t acc[C::kTu][C::kTv];
@@ -378,11 +377,18 @@ struct Fp8Product {
   // behind the first and the second half of the wave's fragments.  (A plain
   // load of them would wait for every load to LDS before it.)  rows: how many
   // the tile has.
+  //
+  // A wave multiplies row after row of fragments while it reads the next one, and
+  // scales each product behind the second one after it.  In front of the last row
+  // all waves meet: what they had of the step is in registers, so that the step's
+  // part of LDS can be filled again, and the next step's fragments are read beside
+  // that row's products.
   template <int PART>
   __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
                                       const char* bp, const float* scale, int blocks, int rows) {
     constexpr int kRowLoads = B::kLoads * PART / C::kTv;
     constexpr int kLoads = A::kLoads + kRowLoads + 1;
+    static_assert((STAGES - 1) * kLoads < 64, "counted by the hardware");
     ra.init(wave % C::kWu * C::kTu * 16);
     rb.init(wave / C::kWu * 16);
 #pragma unroll
@@ -406,10 +412,31 @@ struct Fp8Product {
       scale += AT ? scale_step : 1;
       fill = after(fill);
     };
-    for (int t = 0; t < STAGES - 1 && t < blocks; ++t) start();
+    for (int t = 0; t < STAGES && t < blocks; ++t) start();
+    if (blocks >= STAGES)
+      wait_vm<(STAGES - 1) * kLoads>();
+    else
+      wait_vm<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // Step t is read out and step t + 1 has come, for all waves; then step
+    // t + STAGES takes the place of t.
+    auto meet = [&](int t) {
+      wait_lds();
+      if (t + STAGES <= blocks)
+        wait_vm<(STAGES - 2) * kLoads>();
+      else
+        wait_vm<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (t + STAGES < blocks) start();
+    };
     // the fragments of this wave that hold rows at all
     const int wv = wave / C::kWu;
-    const int nv = min((rows - wv * 16 + C::kWv * 16 - 1) / (C::kWv * 16), C::kTv);
+    if (rows <= wv * 16) {
+      for (int t = 0; t + 1 < blocks; ++t) meet(t);
+      return;
+    }
     // 32 rows of scales every 256 bytes, this wave's two behind its own 32
     const uint32_t scales = A::kBytes + B::kBytes;
     const uint32_t sw_at = scales + wave * 256 + 128;
@@ -418,44 +445,61 @@ struct Fp8Product {
     auto lds_float = [](uint32_t p) {
       return *(const __attribute__((address_space(3))) float*)(uintptr_t)p;
     };
-    for (int t = 0; t < blocks; ++t) {
-      if (t + STAGES - 1 <= blocks)
-        wait_vm<(STAGES - 2) * kLoads>();
-      else
-        wait_vm<0>();
-      wait_lds();  // this wave has read the step before out
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      if (t + STAGES - 1 < blocks) start();
-      if (nv > 0) {
-        const float sw[2] = {lds_float(here + sw_at), lds_float(here + sw_at + 4)};
+    constexpr int kProducts = C::kTu * PART, kBehind = 2, kSlots = kBehind + 1;
+    i32x8_t fa[2], fb[PART];
+    static_assert(kBehind <= (C::kTu - 1) * PART, "a step's scales before the next one's");
+    float sx[PART], sw[2], s[2][PART];
+    f32x4_t part[kSlots];
+    auto read_b = [&](int v) {
+      fb[v] = frag(rb, here + A::kBytes, v * C::kWv);
+      sx[v] = lds_float(here + sx_at + v * C::kWv / 2 * 256);
+    };
+    fa[0] = frag(ra, here, 0);
 #pragma unroll
-        for (int u0 = 0; u0 < C::kTu; u0 += kRows) {
-          i32x8_t fa[kRows];
+    for (int v = 0; v < PART; ++v) read_b(v);
+    sw[0] = lds_float(here + sw_at);
+    sw[1] = lds_float(here + sw_at + 4);
+    // LAST: no step follows.
+    auto step = [&](int t, auto last) {
+      constexpr bool kLast = decltype(last)::value;
 #pragma unroll
-          for (int u = 0; u < kRows; ++u) fa[u] = frag(ra, here, u0 + u);
+      for (int i = 0; i < kProducts + kBehind; ++i) {
+        const int u = i / PART, v = i % PART;
+        if (i < kProducts) {
+          if (v == 0 && u + 1 < C::kTu) fa[(u + 1) % 2] = frag(ra, here, u + 1);
+          if (v == 0 && u + 1 == C::kTu && !kLast) {
+            meet(t);
+            here = after(here);
+            fa[0] = frag(ra, here, 0);
+          }
+          part[i % kSlots] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fa[u % 2], fb[v], f32x4_t{}, 0, 0, 0, 0, 0, 0);
+        }
+        if (i >= kBehind) {
+          const int j = i - kBehind, ju = j / PART, jv = j % PART;
+          if (j == 0) {
 #pragma unroll
-          for (int v = 0; v < PART; ++v) {
-            if (v >= nv) break;
-            const i32x8_t fb = frag(rb, here + A::kBytes, v * C::kWv);
-            const float sx = lds_float(here + sx_at + v * C::kWv / 2 * 256);
-            f32x4_t part[kRows];
+            for (int n = 0; n < 2 * PART; ++n) s[n / PART][n % PART] = sx[n % PART] * sw[n / PART];
+          }
+          const float scale = s[ju / (C::kTu / 2)][jv];
 #pragma unroll
-            for (int u = 0; u < kRows; ++u)
-              part[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[u], fb, f32x4_t{}, 0,
-                                                                         0, 0, 0, 0, 0);
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-              const float s = sx * sw[u0 + u < C::kTu / 2 ? 0 : 1];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[u0 + u][v][i] = fmaf(part[u][i], s, acc[u0 + u][v][i]);
-            }
+          for (int k = 0; k < 4; ++k)
+            acc[ju][jv][k] = fmaf(part[j % kSlots][k], scale, acc[ju][jv][k]);
+          // here and not behind the meeting, where the compiler would move it
+          asm volatile("" : "+v"(acc[ju][jv]));
+        }
+        if (i < kProducts && u + 1 == C::kTu && !kLast) {
+          read_b(v);
+          if (v == 0) {
+            sw[0] = lds_float(here + sw_at);
+            sw[1] = lds_float(here + sw_at + 4);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      here = after(here);
-    }
+    };
+    for (int t = 0; t + 1 < blocks; ++t) step(t, std::false_type{});
+    step(blocks - 1, std::true_type{});
   }
 
   // A tile of `rows` rows: as many quarters (halves) of it as have some.
@@ -480,23 +524,31 @@ struct Fp8Product {
     }
   }
 
+  // AT, behind the last product: lanes 16-31 and 48-63 of a fragment for 0-15 and
+  // 32-47 of its neighbour, which leaves every lane 8 neighbours along u.
+  __device__ __forceinline__ void exchange() {
+    static_assert(AT, "paired fragments need none");
+#pragma unroll
+    for (int v = 0; v < C::kTv; ++v)
+#pragma unroll
+      for (int a = 0; a < C::kTu / 2; ++a) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const auto r = __builtin_amdgcn_permlane16_swap(
+              __float_as_uint(acc[2 * a][v][i]), __float_as_uint(acc[2 * a + 1][v][i]), false,
+              false);
+          acc[2 * a][v][i] = __uint_as_float(r[0]);
+          acc[2 * a + 1][v][i] = __uint_as_float(r[1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  }
+
   // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours along
   // u, from column(a) of the wave's on.
   __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
-    if constexpr (AT) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // lanes 16-31 and 48-63 of the first for 0-15 and 32-47 of the second
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[2 * a][v][i]),
-                                                        __float_as_uint(acc[2 * a + 1][v][i]),
-                                                        false, false);
-        o[i] = __uint_as_float(r[0]);
-        o[4 + i] = __uint_as_float(r[1]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
-    }
+    for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
   }
   static __device__ __forceinline__ int column(int a) {
     const int g = lane_id() >> 4;
