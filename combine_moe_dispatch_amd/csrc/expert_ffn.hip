@@ -109,16 +109,14 @@ ffn_up_kernel(UpParams p, int ntiles) {
   const uint32_t ld = (uint32_t)p.H;
   const int rows = min(C::kBv, t.end - t.m0);
   Product prod;
-  const char* ap[Product::A::kLoads];
-  weight_loads<C, kActSwiglu>(
-      prod.a, ap,
-      reinterpret_cast<const char*>(p.up) + ((size_t)t.e * 2 * p.I + t.n * Cols::kTile) * ld, wave,
-      p.I, p.I - t.n * Cols::kTile, ld);
+  prod.template weight_rows<true>(
+      wave, reinterpret_cast<const char*>(p.up) + ((size_t)t.e * 2 * p.I + t.n * Cols::kTile) * ld,
+      ld, p.I - t.n * Cols::kTile, (size_t)p.I * ld);
   prod.b.init(wave, ld, rows);
   const float* scale =
       lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
                 : p.up_scales + ((size_t)t.e * 2 * ib + t.n + (lane % 2 == 1 ? ib : 0)) * kb;
-  prod.run_rows(smem, wave, ap, reinterpret_cast<const char*>(p.x) + (size_t)t.m0 * ld, scale, kb,
+  prod.run_rows(smem, wave, reinterpret_cast<const char*>(p.x) + (size_t)t.m0 * ld, scale, kb,
                 rows);
   finish_up<C>(prod, p, t, wave, reinterpret_cast<uint32_t*>(smem + Product::kLds));
 }
@@ -221,7 +219,7 @@ __device__ __forceinline__ void finish_slope(const Product& prod, const SlopePar
     uint32_t largest_g = 0, largest_u = 0;
 #pragma unroll
     for (int a = 0; a < kPairs; ++a) {
-      const int col = col0 + Product::column(a);
+      const int col = t.n * C::kBu + Product::column(wu, a);
       float gh[8], g[8], u[8], h[8];
       prod.eight(gh, a, v);
       load8(g, p.pre + at + col);
@@ -248,7 +246,7 @@ __device__ __forceinline__ void finish_slope(const Product& prod, const SlopePar
     if (!there) continue;
 #pragma unroll
     for (int a = 0; a < kPairs; ++a) {
-      const int col = col0 + Product::column(a);
+      const int col = t.n * C::kBu + Product::column(wu, a);
       *reinterpret_cast<uint2*>(p.gz + at + col) = gate.codes(dg[a]);
       *reinterpret_cast<uint2*>(p.gz + at + p.I + col) = up.codes(du[a]);
     }
@@ -269,22 +267,19 @@ __device__ __forceinline__ void transposed_product(Product& prod, char* smem, co
                                                    const float* weight_scales, int red, int cols) {
   const int lane = lane_id(), rb = red / kFp8Block, cb = cols / kFp8Block, n0 = t.n * C::kBu;
   const int rows = min(C::kBv, t.end - t.m0);
-  const char* ap[Product::A::kLoads];
-#pragma unroll
-  for (int i = 0; i < Product::A::kLoads; ++i)
-    ap[i] = reinterpret_cast<const char*>(weight) + (size_t)t.e * red * cols + n0;
-  prod.a_step = (size_t)kFp8Block * cols;
-  prod.a.init(wave, (uint32_t)cols, min(C::kBu, cols - n0));
+  prod.weight_columns(wave, reinterpret_cast<const char*>(weight) + (size_t)t.e * red * cols + n0,
+                      (uint32_t)cols, cols - n0);
   prod.b.init(wave, (uint32_t)red, rows);
-  // a wave's columns lie in one block of scales; past the last column any will do
-  static_assert(C::kTu * 16 <= kFp8Block, "one scale a wave");
-  const int block = min(n0 + wave % C::kWu * (C::kTu * 16), cols - 1) / kFp8Block;
+  // half a wave's columns lie in one block of scales; past the last column any will do
+  static_assert(kFp8Block % Product::kHalfRows == 0, "one scale half a wave");
+  const int block =
+      min(n0 + Product::place(lane % 2, wave % C::kWu * Product::kHalfRows), cols - 1) / kFp8Block;
   const float* scale =
       lane < 32 ? row_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * rb
                 : weight_scales + (size_t)t.e * rb * cb + block;
   prod.scale_step = lane < 32 ? 1 : cb;
-  prod.run_rows(smem, wave, ap, reinterpret_cast<const char*>(rows_codes) + (size_t)t.m0 * red,
-                scale, rb, rows);
+  prod.run_rows(smem, wave, reinterpret_cast<const char*>(rows_codes) + (size_t)t.m0 * red, scale,
+                rb, rows);
   prod.exchange();
 }
 
@@ -314,7 +309,7 @@ struct RowGradParams {
 template <class C>
 __global__ void __launch_bounds__(C::kThreads)
 ffn_grad_x_kernel(RowGradParams p, int ntiles) {
-  using Product = Fp8Product<C, kStages<C>, true>;
+  using Product = Fp8Product<C, kStages<C>, true, true>;
   extern __shared__ __align__(1024) char smem[];
   Tile t;
   if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
@@ -327,7 +322,7 @@ ffn_grad_x_kernel(RowGradParams p, int ntiles) {
     const int m = t.m0 + (v * C::kWv + wv) * 16 + (lane & 15);
 #pragma unroll
     for (int a = 0; a < C::kTu / 2; ++a) {
-      const int col = t.n * C::kBu + wu * (C::kTu * 16) + Product::column(a);
+      const int col = t.n * C::kBu + Product::column(wu, a);
       float o[8];
       prod.eight(o, a, v);
       if (m < t.end && col < p.H) store8(p.grad_x + (size_t)m * p.H + col, o);

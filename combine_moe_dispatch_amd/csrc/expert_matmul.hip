@@ -357,10 +357,9 @@ matmul_fp8_kernel(MatmulParams p, int ntiles) {
   const uint32_t ld = (uint32_t)p.K;
   const int rows = min(C::kBv, t.end - t.m0);
   Product prod;
-  const char* ap[Product::A::kLoads];
-  weight_loads<C, ACT>(prod.a, ap,
-                       static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld, wave,
-                       p.F, p.F - n0, ld);
+  prod.template weight_rows<Cols::kGated>(
+      wave, static_cast<const char*>(p.weight) + ((size_t)t.e * p.P + n0) * ld, ld, p.F - n0,
+      (size_t)p.F * ld);
   prod.b.init(wave, ld, rows);
   // the scales of this wave's weight rows (all of one block of 128, or of the
   // gate's and the up's block); past the last column any will do
@@ -372,7 +371,7 @@ matmul_fp8_kernel(MatmulParams p, int ntiles) {
       lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
                 : p.weight_scales + ((size_t)t.e * (p.P / 128) + block + up) * kb;
   const char* bp = static_cast<const char*>(p.x) + (size_t)t.m0 * ld;
-  prod.run_rows(smem, wave, ap, bp, scale, kb, rows);
+  prod.run_rows(smem, wave, bp, scale, kb, rows);
   finish<C, ACT>(prod, p, t, wave);
 }
 

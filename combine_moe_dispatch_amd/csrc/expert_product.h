@@ -252,9 +252,9 @@ struct TileProduct {
 };
 
 // ---------------------------------------------------------------------------
-// An e4m3 operand held transposed: one step is 128 rows along r of SIZE columns,
-// [128][SIZE] bytes in LDS, read back through the transposing 8-byte load: of 16
-// lanes, lane j names 8 bytes of row j / 2 (columns 0-7 or 8-15) and receives
+// Half of an e4m3 operand held transposed: one step is 128 rows along r of SIZE
+// columns, [128][SIZE] bytes in LDS, read back through the transposing 8-byte load:
+// of 16 lanes, lane j names 8 bytes of row j / 2 (columns 0-7 or 8-15) and receives
 // column j of the 8 rows.  As in OperandTile the layout is linear in the lanes and
 // chunk c of row i sits in slot c ^ f(i): the 16 rows that half a wave reads from
 // (two runs of 8, 16 apart) take 16 different places of the 256 bytes of banks.
@@ -266,25 +266,20 @@ struct TransposedCodes {
   static constexpr int kBytes = SIZE * 128;
   static constexpr int kLoads = kBytes / 1024 / WAVES;
   static_assert(kLoads * WAVES * 1024 == kBytes, "whole wave loads");
-  static_assert(SIZE == 256, "the swizzle is that of rows of 256 bytes");
+  static_assert(SIZE == 128, "the swizzle is that of rows of 128 bytes");
   static constexpr int kSlots = SIZE / 16;
   static constexpr int kRowsPerLoad = 64 / kSlots;
   uint32_t off[kLoads];
 
   static __device__ __forceinline__ int swizzle(int row) {
-    return (row & 7) | ((row >> 4) & 1) << 3;
+    return ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
   }
   static __device__ __forceinline__ int load_of(int i, int wave) { return i * WAVES + wave; }
-  // ld: bytes between rows.  valid: columns the tile really has (a multiple of
-  // 16); past them the last ones are read again.
-  __device__ __forceinline__ void init(int wave, uint32_t ld, int valid) {
+  // The chunk that this lane brings in with load q, and its row.
+  static __device__ __forceinline__ void chunk_of(int q, int& row, int& c) {
     const int lane = lane_id();
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = load_of(i, wave) * kRowsPerLoad + lane / kSlots;
-      const int c = (lane % kSlots) ^ swizzle(row);
-      off[i] = (uint32_t)row * ld + (uint32_t)min(c * 16, valid - 16);
-    }
+    row = q * kRowsPerLoad + lane / kSlots;
+    c = (lane % kSlots) ^ swizzle(row);
   }
   template <bool TAIL>
   __device__ __forceinline__ void load(int i, uint32_t lds, int wave, const char* base, uint32_t,
@@ -337,25 +332,69 @@ struct TransposedCodes {
 //
 // AT: A is held transposed, its rows along r.  Its fragments are not paired, so
 // that a lane's eight neighbours come from an exchange between the lanes behind
-// the last product.
+// the last product.  ACROSS: the waves' first fragments are the tile's first
+// half, which is read in whole lines (rows' gradient of 2048 tokens 558 us against
+// 610); otherwise a wave has neighbouring columns.
 // ---------------------------------------------------------------------------
-template <class C, int STAGES, bool AT = false>
+template <class C, int STAGES, bool AT = false, bool ACROSS = false>
 struct Fp8Product {
-  using A = std::conditional_t<AT, TransposedCodes<C::kBu, C::kWaves>,
-                               OperandTile<C::kBu, C::kWaves, false, true>>;
+  // A lies in two halves: of every wave's fragments the first ones, then the others.
+  using Half = std::conditional_t<AT, TransposedCodes<C::kBu / 2, C::kWaves>,
+                                  OperandTile<C::kBu / 2, C::kWaves, false, true>>;
   using B = OperandTile<C::kBv, C::kWaves, false, false>;
+  static constexpr int kHalf = C::kTu / 2, kHalfRows = kHalf * 16;  // of a wave
   static constexpr int kScales = C::kWaves * 256;  // one dword a lane
   static_assert(C::kBv <= C::kWaves * 32, "a wave brings in the scales of 32 rows");
-  static constexpr int kStage = A::kBytes + B::kBytes + kScales;
+  static constexpr int kStage = 2 * Half::kBytes + B::kBytes + kScales;
   static constexpr int kLds = STAGES * kStage;
-  A a;
+  Half a[2];
   B b;
   f32x4_t acc[C::kTu][C::kTv];
-  typename A::template Reader<C::kTu> ra;
+  typename Half::template Reader<kHalf> ra;
   typename B::template Reader<C::kTv> rb;
+  const char* ap[2];  // the halves' first step,
+  size_t a_step;      // the bytes to the next one (AT),
+  int scale_step;     // and the entries between this lane's scales (AT)
 
-  size_t a_step;   // AT: bytes between the steps of A,
-  int scale_step;  // and entries between this lane's scales
+  // Position along u of place i of a half, in the tile.
+  static __device__ __forceinline__ int place(int half, int i) {
+    if (ACROSS) return half * (C::kBu / 2) + i;
+    return i / kHalfRows * (2 * kHalfRows) + half * kHalfRows + i % kHalfRows;
+  }
+  // Weight rows w, w + ld, .. of which cols are left; GATED: the first halves are
+  // gate rows, the second ones the up rows of the same columns, up bytes on.
+  template <bool GATED>
+  __device__ __forceinline__ void weight_rows(int wave, const char* w, uint32_t ld, int cols,
+                                              size_t up) {
+    static_assert(!AT, "rows along r");
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < Half::kLoads; ++i) {
+        int row, c;
+        Half::chunk_of(Half::load_of(i, wave), row, c);
+        const int col = GATED ? row : place(half, row);
+        a[half].off[i] = (uint32_t)min(col, cols - 1) * ld + (uint32_t)c * 16;
+        a[half].where[i] = 0;
+      }
+      ap[half] = w + (GATED && half == 1 ? up : 0);
+    }
+  }
+  // Weight columns w, w + 1, .. of which cols are left (a multiple of 16).
+  __device__ __forceinline__ void weight_columns(int wave, const char* w, uint32_t ld, int cols) {
+    static_assert(AT, "rows along u");
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < Half::kLoads; ++i) {
+        int row, c;
+        Half::chunk_of(Half::load_of(i, wave), row, c);
+        a[half].off[i] = (uint32_t)row * ld + (uint32_t)min(place(half, c * 16), cols - 16);
+      }
+      ap[half] = w;
+    }
+    a_step = (size_t)kFp8Block * ld;
+  }
 
   template <class R>
   static __device__ __forceinline__ i32x8_t frag(const R& r, uint32_t lds, int n) {
@@ -372,108 +411,168 @@ struct Fp8Product {
     }
   }
 
-  // PART: as in TileProduct.  blocks > 0 steps.  scale: the scale this lane brings in, of step 0: lanes
-  // 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of the weight rows
-  // behind the first and the second half of the wave's fragments.  (A plain
-  // load of them would wait for every load to LDS before it.)  rows: how many
-  // the tile has.
+  // PART: as in TileProduct.  blocks > 0 steps.  scale: the scale this lane brings
+  // in, of step 0: lanes 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of
+  // the weight rows behind the first and the second half of the wave's fragments.
+  // (A plain load of them would wait for every load to LDS before it.)  rows: how
+  // many the tile has.
   //
   // A wave multiplies row after row of fragments while it reads the next one, and
-  // scales each product behind the second one after it.  In front of the last row
-  // all waves meet: what they had of the step is in registers, so that the step's
-  // part of LDS can be filled again, and the next step's fragments are read beside
-  // that row's products.
+  // scales each product behind the second one after it.  B's fragments stay in
+  // registers for a step.  All waves meet twice a step: in front of the last row of
+  // A's first half, when that half, B and the scales are in registers and their
+  // place can be filled again, and in front of the last row, for the second half.
+  // So a load has one and a half steps to arrive with two steps of LDS (with one
+  // meeting a step, and one step to arrive, 4096 tokens' up projections took 955
+  // us, XXX now; without any wait for memory YYY).
   template <int PART>
-  __device__ __forceinline__ void run(char* smem, int wave, const char* (&ap)[A::kLoads],
-                                      const char* bp, const float* scale, int blocks, int rows) {
+  __device__ __forceinline__ void run(char* smem, int wave, const char* bp, const float* scale,
+                                      int blocks, int rows) {
     constexpr int kRowLoads = B::kLoads * PART / C::kTv;
-    constexpr int kLoads = A::kLoads + kRowLoads + 1;
-    static_assert((STAGES - 1) * kLoads < 64, "counted by the hardware");
-    ra.init(wave % C::kWu * C::kTu * 16);
+    constexpr int kFirst = Half::kLoads + kRowLoads + 1;  // loads of a first half, B and scales
+    constexpr int kSecond = Half::kLoads;
+    constexpr int kLoads = kFirst + kSecond;
+    static_assert((STAGES - 1) * kLoads + kSecond < 64, "counted by the hardware");
+    constexpr uint32_t kSecondAt = Half::kBytes, kRowsAt = 2 * Half::kBytes,
+                       kScalesAt = kRowsAt + B::kBytes;
+    ra.init(wave % C::kWu * kHalfRows);
     rb.init(wave / C::kWu * 16);
 #pragma unroll
     for (int u = 0; u < C::kTu; ++u)
 #pragma unroll
       for (int v = 0; v < C::kTv; ++v) acc[u][v] = f32x4_t{};
     const uint32_t lds = lds_address(smem), lds_end = lds + kLds;
-    uint32_t fill = lds, here = lds;
+    uint32_t here = lds;
     auto after = [&](uint32_t slot) { return slot + kStage == lds_end ? lds : slot + kStage; };
-    auto start = [&] {
-#pragma unroll
-      for (int i = 0; i < A::kLoads; ++i) {
-        a.template load<false>(i, fill, wave, ap[i], 0, 0);
-        ap[i] += AT ? a_step : 128;
+    auto load_first = [&](int i, uint32_t slot) {
+      if (i < Half::kLoads) {
+        a[0].template load<false>(i, slot, wave, ap[0], 0, 0);
+      } else if (i + 1 < kFirst) {
+        b.template load<false>(i - Half::kLoads, slot + kRowsAt, wave, bp, 0, 0);
+      } else {
+        load4_to_lds(slot + kScalesAt + wave * 256, scale);
+        ap[0] += AT ? a_step : 128;
+        bp += 128;
+        scale += AT ? scale_step : 1;
       }
-#pragma unroll
-      for (int i = 0; i < kRowLoads; ++i)
-        b.template load<false>(i, fill + A::kBytes, wave, bp, 0, 0);
-      load4_to_lds(fill + A::kBytes + B::kBytes + wave * 256, scale);
-      bp += 128;
-      scale += AT ? scale_step : 1;
-      fill = after(fill);
     };
-    for (int t = 0; t < STAGES && t < blocks; ++t) start();
+    auto start_first = [&](uint32_t slot) {
+#pragma unroll
+      for (int i = 0; i < kFirst; ++i) load_first(i, slot);
+    };
+    auto start_second = [&](uint32_t slot) {
+#pragma unroll
+      for (int i = 0; i < kSecond; ++i)
+        a[1].template load<false>(i, slot + kSecondAt, wave, ap[1], 0, 0);
+      ap[1] += AT ? a_step : 128;
+    };
+    for (int t = 0; t < STAGES && t < blocks; ++t) {
+      start_first(here);
+      start_second(here);
+      here = after(here);
+    }
+    here = lds;
     if (blocks >= STAGES)
-      wait_vm<(STAGES - 1) * kLoads>();
+      wait_vm<(STAGES - 1) * kLoads + kSecond>();
     else
       wait_vm<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    // Step t is read out and step t + 1 has come, for all waves; then step
-    // t + STAGES takes the place of t.
-    auto meet = [&](int t) {
+    // All waves have read the first half, B and the scales of step t out, and its
+    // second half has come.
+    auto meet_first = [&](int t) {
       wait_lds();
       if (t + STAGES <= blocks)
-        wait_vm<(STAGES - 2) * kLoads>();
+        wait_vm<(STAGES - 1) * kLoads>();
       else
         wait_vm<0>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      if (t + STAGES < blocks) start();
+    };
+    // They have read its second half out, and what step t + 1 begins with has come.
+    auto meet_second = [&](int t) {
+      wait_lds();
+      if (t + STAGES < blocks)
+        wait_vm<(STAGES - 1) * kLoads>();
+      else if (t + STAGES == blocks)
+        wait_vm<(STAGES - 2) * kLoads + kSecond>();
+      else
+        wait_vm<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
     };
     // the fragments of this wave that hold rows at all
     const int wv = wave / C::kWu;
     if (rows <= wv * 16) {
-      for (int t = 0; t + 1 < blocks; ++t) meet(t);
+      for (int t = 0; t < blocks; ++t) {
+        meet_first(t);
+        if (t + STAGES < blocks) start_first(here);
+        if (t + 1 == blocks) break;
+        meet_second(t);
+        if (t + STAGES < blocks) start_second(here);
+        here = after(here);
+      }
       return;
     }
     // 32 rows of scales every 256 bytes, this wave's two behind its own 32
-    const uint32_t scales = A::kBytes + B::kBytes;
-    const uint32_t sw_at = scales + wave * 256 + 128;
-    const uint32_t sx_at = scales + wv / 2 * 256 + wv % 2 * 64 + (lane_id() & 15) * 4;
+    const uint32_t sw_at = kScalesAt + wave * 256 + 128;
+    const uint32_t sx_at = kScalesAt + wv / 2 * 256 + wv % 2 * 64 + (lane_id() & 15) * 4;
     static_assert(C::kWv % 2 == 0, "a fragment's scales lie 256 bytes per two fragments on");
     auto lds_float = [](uint32_t p) {
       return *(const __attribute__((address_space(3))) float*)(uintptr_t)p;
     };
     constexpr int kProducts = C::kTu * PART, kBehind = 2, kSlots = kBehind + 1;
-    i32x8_t fa[2], fb[PART];
     static_assert(kBehind <= (C::kTu - 1) * PART, "a step's scales before the next one's");
+    i32x8_t fa[2], fb[PART];
     float sx[PART], sw[2], s[2][PART];
     f32x4_t part[kSlots];
+    auto read_a = [&](int u) {
+      fa[u % 2] = frag(ra, here + u / kHalf * kSecondAt, u % kHalf);
+    };
     auto read_b = [&](int v) {
-      fb[v] = frag(rb, here + A::kBytes, v * C::kWv);
+      fb[v] = frag(rb, here + kRowsAt, v * C::kWv);
       sx[v] = lds_float(here + sx_at + v * C::kWv / 2 * 256);
     };
-    fa[0] = frag(ra, here, 0);
+    read_a(0);
 #pragma unroll
     for (int v = 0; v < PART; ++v) read_b(v);
     sw[0] = lds_float(here + sw_at);
     sw[1] = lds_float(here + sw_at + 4);
+    // A first half's loads are started some with each row of products: all at once
+    // they hold up the waves.
+    constexpr int kSpread = kHalf - 1 < 3 ? kHalf - 1 : 3;
+    constexpr int kChunk = (kFirst + kSpread - 1) / kSpread;
+    static_assert(kSpread > 0 && kHalf % 2 == 0, "all before the next meeting, in two buffers");
     // LAST: no step follows.
     auto step = [&](int t, auto last) {
       constexpr bool kLast = decltype(last)::value;
+      const bool more = !kLast && t + STAGES < blocks;
+      const uint32_t slot = here;
 #pragma unroll
       for (int i = 0; i < kProducts + kBehind; ++i) {
         const int u = i / PART, v = i % PART;
-        if (i < kProducts) {
-          if (v == 0 && u + 1 < C::kTu) fa[(u + 1) % 2] = frag(ra, here, u + 1);
-          if (v == 0 && u + 1 == C::kTu && !kLast) {
-            meet(t);
+        const bool row = i < kProducts && v == 0;
+        if (row) {
+          if (u + 1 == kHalf) meet_first(t);
+          if (u + 1 < C::kTu) {
+            read_a(u + 1);
+          } else if (!kLast) {
+            meet_second(t);
             here = after(here);
-            fa[0] = frag(ra, here, 0);
+            read_a(0);
           }
+        }
+        if (i < kProducts)
           part[i % kSlots] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
               fa[u % 2], fb[v], f32x4_t{}, 0, 0, 0, 0, 0, 0);
+        if (row && more) {
+          const int n = u + 1 - kHalf;
+          if (n >= 0 && n < kSpread) {
+#pragma unroll
+            for (int q = 0; q < kChunk; ++q)
+              if (n * kChunk + q < kFirst) load_first(n * kChunk + q, slot);
+          }
+          if (u + 1 == C::kTu) start_second(slot);
         }
         if (i >= kBehind) {
           const int j = i - kBehind, ju = j / PART, jv = j % PART;
@@ -481,11 +580,11 @@ struct Fp8Product {
 #pragma unroll
             for (int n = 0; n < 2 * PART; ++n) s[n / PART][n % PART] = sx[n % PART] * sw[n / PART];
           }
-          const float scale = s[ju / (C::kTu / 2)][jv];
+          const float scale = s[ju / kHalf][jv];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             acc[ju][jv][k] = fmaf(part[j % kSlots][k], scale, acc[ju][jv][k]);
-          // here and not behind the meeting, where the compiler would move it
+          // here and not behind a meeting, where the compiler would move it
           asm volatile("" : "+v"(acc[ju][jv]));
         }
         if (i < kProducts && u + 1 == C::kTu && !kLast) {
@@ -503,24 +602,23 @@ struct Fp8Product {
   }
 
   // A tile of `rows` rows: as many quarters (halves) of it as have some.
-  __device__ __forceinline__ void run_rows(char* smem, int wave, const char* (&ap)[A::kLoads],
-                                           const char* bp, const float* scale, int blocks,
-                                           int rows) {
+  __device__ __forceinline__ void run_rows(char* smem, int wave, const char* bp,
+                                           const float* scale, int blocks, int rows) {
     if constexpr (C::kTv % 4 == 0) {
       if (rows > C::kBv * 3 / 4)
-        run<C::kTv>(smem, wave, ap, bp, scale, blocks, rows);
+        run<C::kTv>(smem, wave, bp, scale, blocks, rows);
       else if (rows > C::kBv / 2)
-        run<C::kTv * 3 / 4>(smem, wave, ap, bp, scale, blocks, rows);
+        run<C::kTv * 3 / 4>(smem, wave, bp, scale, blocks, rows);
       else if (rows > C::kBv / 4)
-        run<C::kTv / 2>(smem, wave, ap, bp, scale, blocks, rows);
+        run<C::kTv / 2>(smem, wave, bp, scale, blocks, rows);
       else
-        run<C::kTv / 4>(smem, wave, ap, bp, scale, blocks, rows);
+        run<C::kTv / 4>(smem, wave, bp, scale, blocks, rows);
     } else {
       static_assert(C::kTv % 2 == 0 && B::kLoads % 2 == 0, "whole loads of half a tile");
       if (rows > C::kBv / 2)
-        run<C::kTv>(smem, wave, ap, bp, scale, blocks, rows);
+        run<C::kTv>(smem, wave, bp, scale, blocks, rows);
       else
-        run<C::kTv / 2>(smem, wave, ap, bp, scale, blocks, rows);
+        run<C::kTv / 2>(smem, wave, bp, scale, blocks, rows);
     }
   }
 
@@ -545,14 +643,15 @@ struct Fp8Product {
   }
 
   // This lane's outputs of fragments 2a and 2a + 1 by v: eight neighbours along
-  // u, from column(a) of the wave's on.
+  // u, from column(wu, a) of the tile on.
   __device__ __forceinline__ void eight(float (&o)[8], int a, int v) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = acc[2 * a + i / 4][v][i % 4];
   }
-  static __device__ __forceinline__ int column(int a) {
+  static __device__ __forceinline__ int column(int wu, int a) {
     const int g = lane_id() >> 4;
-    return a * 32 + (AT ? (g & 1) * 16 + (g >> 1) * 8 : g * 8);
+    return place(a * 2 / kHalf, wu * kHalfRows) + a * 2 % kHalf * 16 +
+           (AT ? (g & 1) * 16 + (g >> 1) * 8 : g * 8);
   }
 };
 
