@@ -26,40 +26,42 @@ __device__ __forceinline__ uint32_t max_over_16(uint32_t m) {
 }
 
 // The scale of a block whose largest magnitude is given, and its codes.
+//
+// v / scale without a division: from the correctly rounded reciprocal r,
+// q0 = v r and one remainder correction q0 + r (v - scale q0), both fused, give the
+// correctly rounded quotient when nothing underflows (Markstein's division).
+// Scales far from 1 are first brought near it, with the values, by a power of two,
+// which is exact; then only quotients that round to code 0 can underflow.
+// |q| <= 448 (1 + 2^-23)^2, which the packed convert rounds to nearest even, but
+// for scales below 2^-126, which are too coarse: those quotients are cut at 448.
 struct BlockScale {
-  float scale, inverse;
-  bool ordinary;
+  float scale, factor, by, inverse;
 
   __device__ __forceinline__ explicit BlockScale(uint32_t largest) {
     scale = __uint_as_float(largest) / 448.0f;
-    inverse = 1.0f / scale;
-    ordinary = scale >= 0x1p-80f && scale <= 0x1p80f;
-  }
-
-  // v / scale without a division: from the correctly rounded reciprocal r,
-  // q0 = v r and one remainder correction q0 + r (v - scale q0), both fused,
-  // give the correctly rounded quotient when nothing underflows (Markstein's
-  // division).  In the ordinary range only quotients that round to code 0 can;
-  // |q| <= 448 (1 + 2^-23)^2, which the packed convert rounds to nearest even.
-  __device__ __forceinline__ float quotient(float v) const {
-    const float q0 = v * inverse;
-    return fmaf(fmaf(-scale, q0, v), inverse, q0);
+    factor = scale < 0x1p-80f ? 0x1p100f : scale > 0x1p80f ? 0x1p-100f : 1.0f;
+    by = scale * factor;
+    inverse = scale == 0.0f ? 0.0f : 1.0f / by;
+    if (by == __builtin_inff()) by = 0.0f;  // then inverse is 0, and inf * 0 a NaN
   }
 
   // Eight neighbouring codes.
   __device__ __forceinline__ uint2 codes(const float (&v)[8]) const {
-    uint32_t c[2] = {0, 0};
-    if (ordinary) {
+    float q[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[4 * i]), quotient(v[4 * i + 1]),
-                                                       0, false);
-        c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[4 * i + 2]),
-                                                         quotient(v[4 * i + 3]), lo, true);
-      }
-    } else if (scale != 0.0f) {  // very small or large, infinite or NaN
+    for (int i = 0; i < 8; ++i) {
+      const float x = v[i] * factor, q0 = x * inverse;
+      q[i] = fmaf(fmaf(-by, q0, x), inverse, q0);
+    }
+    if (scale < 0x1p-126f) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i / 4] |= f32_to_e4m3(v[i] / scale) << (8 * (i % 4));
+      for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(q[i], -448.0f), 448.0f);
+    }
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
+      c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], lo, true);
     }
     return make_uint2(c[0], c[1]);
   }
