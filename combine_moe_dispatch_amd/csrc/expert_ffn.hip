@@ -21,10 +21,11 @@ namespace moe {
 namespace {
 
 // 256 columns of u by 256 token rows in two steps of LDS (Codes), or by 128 in
-// three.
+// three.  NarrowCodes: 128 by 128, two blocks to a compute unit.
 using ShortCodes = Config<2, 4, 8, 2>;
+using NarrowCodes = Config<2, 4, 4, 2>;
 template <class C>
-constexpr int kStages = C::kTv == 4 ? 2 : 3;
+constexpr int kStages = C::kTv == 4 || C::kTu == 4 ? 2 : 3;
 
 // ---------------------------------------------------------------------------
 // Forward: h
@@ -66,7 +67,7 @@ __device__ __forceinline__ void finish_up(Product& prod, const UpParams& p, cons
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        z[i] = z[i] * sigmoid_f32(z[i]) * up[i];
+        z[i] = z[i] * sigmoid_short(z[i]) * up[i];
         largest = max(largest, magnitude(z[i]));
         prod.acc[2 * a + i / 4][v][i % 4] = z[i];
       }
@@ -93,6 +94,26 @@ __device__ __forceinline__ void finish_up(Product& prod, const UpParams& p, cons
   }
 }
 
+template <class C, class Product>
+__device__ __forceinline__ void up_product(Product& prod, char* smem, const UpParams& p,
+                                           const Tile& t, int wave) {
+  using Cols = Columns<C, kActSwiglu>;
+  const int kb = p.H / kFp8Block, ib = p.I / kFp8Block, lane = lane_id();
+  const int n0 = t.n * Cols::kTile;
+  const uint32_t ld = (uint32_t)p.H;
+  const int rows = min(C::kBv, t.end - t.m0);
+  prod.template weight_rows<true>(
+      wave, reinterpret_cast<const char*>(p.up) + ((size_t)t.e * 2 * p.I + n0) * ld, ld, p.I - n0,
+      (size_t)p.I * ld);
+  prod.b.init(wave, ld, rows);
+  const float* scale =
+      lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
+                : p.up_scales +
+                      ((size_t)t.e * 2 * ib + n0 / kFp8Block + (lane % 2 == 1 ? ib : 0)) * kb;
+  prod.run_rows(smem, wave, reinterpret_cast<const char*>(p.x) + (size_t)t.m0 * ld, scale, kb,
+                rows);
+}
+
 template <class C>
 constexpr int kUpLds = Fp8Product<C, kStages<C>>::kLds + C::kWu * C::kBv * 4;
 
@@ -100,25 +121,134 @@ template <class C>
 __global__ void __launch_bounds__(C::kThreads)
 ffn_up_kernel(UpParams p, int ntiles) {
   using Product = Fp8Product<C, kStages<C>>;
-  using Cols = Columns<C, kActSwiglu>;
+  extern __shared__ __align__(1024) char smem[];
+  Tile t;
+  if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  Product prod;
+  up_product<C>(prod, smem, p, t, wave);
+  finish_up<C>(prod, p, t, wave, reinterpret_cast<uint32_t*>(smem + Product::kLds));
+}
+
+// ---------------------------------------------------------------------------
+// Few tiles: the steps of a tile are shared out over the blocks of gridDim.y, whose
+// sums lie behind one another in fp32; a launch of its own adds them up and does
+// what comes after the product.  One token's way through one expert is its weights'
+// way from memory, and 32 tiles of 56 steps would leave that to 32 compute units.
+// ---------------------------------------------------------------------------
+struct SplitParams {
+  Segments seg;
+  const uint8_t* x;
+  const float* x_scales;
+  const uint8_t* weight;
+  const float* weight_scales;
+  float* parts;  // [gridDim.y][seg.rows][P]
+  int K, P;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+ffn_split_kernel(SplitParams p, int ntiles) {
+  using Product = Fp8Product<C, kStages<C>>;
+  static_assert(C::kBu == kFp8Block, "a tile's weight rows are one block of scales");
   extern __shared__ __align__(1024) char smem[];
   Tile t;
   if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
-  const int kb = p.H / kFp8Block, ib = p.I / kFp8Block;
-  const uint32_t ld = (uint32_t)p.H;
-  const int rows = min(C::kBv, t.end - t.m0);
+  const int kb = p.K / kFp8Block, rows = min(C::kBv, t.end - t.m0);
+  // every share has a step (the launch sees to that)
+  const int first = (int)((int64_t)kb * blockIdx.y / gridDim.y);
+  const int last = (int)((int64_t)kb * (blockIdx.y + 1) / gridDim.y);
+  const uint32_t ld = (uint32_t)p.K;
   Product prod;
-  prod.template weight_rows<true>(
-      wave, reinterpret_cast<const char*>(p.up) + ((size_t)t.e * 2 * p.I + t.n * Cols::kTile) * ld,
-      ld, p.I - t.n * Cols::kTile, (size_t)p.I * ld);
+  prod.template weight_rows<false>(
+      wave,
+      reinterpret_cast<const char*>(p.weight) + ((size_t)t.e * p.P + t.n * C::kBu) * ld +
+          first * kFp8Block,
+      ld, p.P - t.n * C::kBu, 0);
   prod.b.init(wave, ld, rows);
   const float* scale =
       lane < 32 ? p.x_scales + (size_t)(t.m0 + min(wave * 32 + lane, rows - 1)) * kb
-                : p.up_scales + ((size_t)t.e * 2 * ib + t.n + (lane % 2 == 1 ? ib : 0)) * kb;
-  prod.run_rows(smem, wave, reinterpret_cast<const char*>(p.x) + (size_t)t.m0 * ld, scale, kb,
-                rows);
-  finish_up<C>(prod, p, t, wave, reinterpret_cast<uint32_t*>(smem + Product::kLds));
+                : p.weight_scales + ((size_t)t.e * (p.P / kFp8Block) + t.n) * kb;
+  prod.run_rows(smem, wave,
+                reinterpret_cast<const char*>(p.x) + (size_t)t.m0 * ld + first * kFp8Block,
+                scale + first, last - first, rows);
+  const int wu = wave % C::kWu, wv = wave / C::kWu;
+#pragma unroll
+  for (int v = 0; v < C::kTv; ++v) {
+    const int m = t.m0 + (v * C::kWv + wv) * 16 + (lane & 15);
+    if (m >= t.end) continue;
+    float* out = p.parts + ((size_t)blockIdx.y * p.seg.rows + m) * p.P + t.n * C::kBu;
+#pragma unroll
+    for (int a = 0; a < C::kTu / 2; ++a) {
+      float o[8];
+      prod.eight(o, a, v);
+      float4* q = reinterpret_cast<float4*>(out + Product::column(wu, a));
+      q[0] = make_float4(o[0], o[1], o[2], o[3]);
+      q[1] = make_float4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+// Eight neighbouring sums of a row from their shares, in the shares' order.
+__device__ __forceinline__ void add_shares(float (&v)[8], const float* parts, size_t apart,
+                                           int shares) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < shares; ++s) add8(v, parts + s * apart);
+}
+
+constexpr int kJoinRows = 4, kJoinThreads = 256;
+
+// h and its 8 bits from the shares of z.
+__global__ void __launch_bounds__(kJoinThreads)
+ffn_join_up_kernel(UpParams p, const float* parts, int shares) {
+  Tile t;
+  if (!find_tile<kJoinRows>(p.seg, 1, blockIdx.x, t)) return;
+  const int rows = min(kJoinRows, t.end - t.m0), units = p.I / 8;
+  const size_t apart = (size_t)p.seg.rows * (2 * p.I);
+  // units per row are a multiple of 16: the 16 lanes of a scale block stay together
+  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * units;
+       i += gridDim.y * kJoinThreads) {
+    const size_t m = t.m0 + i / units;
+    const int c = i % units * 8;
+    const float* z = parts + m * (2 * p.I) + c;
+    float g[8], u[8];
+    add_shares(g, z, apart, shares);
+    add_shares(u, z + p.I, apart, shares);
+    if (p.pre) {
+      store8(p.pre + m * (2 * p.I) + c, g);
+      store8(p.pre + m * (2 * p.I) + p.I + c, u);
+    }
+    uint32_t largest = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      g[j] = g[j] * sigmoid_short(g[j]) * u[j];
+      largest = max(largest, magnitude(g[j]));
+    }
+    const BlockScale block(max_over_16(largest));
+    const size_t at = m * p.I + c;
+    *reinterpret_cast<uint2*>(p.h + at) = block.codes(g);
+    if (threadIdx.x % 16 == 0) p.h_scales[at / kFp8Block] = block.scale;
+  }
+}
+
+// y from its shares.
+__global__ void __launch_bounds__(kJoinThreads)
+ffn_join_down_kernel(Segments seg, const float* parts, int shares, const uint16_t* residual,
+                     uint16_t* y, int H) {
+  Tile t;
+  if (!find_tile<kJoinRows>(seg, 1, blockIdx.x, t)) return;
+  const int rows = min(kJoinRows, t.end - t.m0), units = H / 8;
+  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * units;
+       i += gridDim.y * kJoinThreads) {
+    const size_t at = (size_t)t.m0 * H + (size_t)i * 8;
+    float v[8];
+    add_shares(v, parts + at, (size_t)seg.rows * H, shares);
+    if (residual) add8(v, residual + at);
+    store8(y + at, v);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -180,7 +310,7 @@ ffn_hidden_kernel(Segments seg, const uint16_t* pre, uint16_t* h, int I) {
     load8(g, pre + m * (2 * I) + c);
     load8(u, pre + m * (2 * I) + I + c);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = g[j] * sigmoid_f32(g[j]) * u[j];
+    for (int j = 0; j < 8; ++j) g[j] = g[j] * sigmoid_short(g[j]) * u[j];
     store8(h + m * I + c, g);
   }
 }
@@ -226,7 +356,7 @@ __device__ __forceinline__ void finish_slope(const Product& prod, const SlopePar
       load8(u, p.pre + at + p.I + col);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = sigmoid_f32(g[i]);
+        const float s = sigmoid_short(g[i]);
         const float silu = g[i] * s;
         dg[a][i] = gh[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
         du[a][i] = gh[i] * silu;
@@ -366,25 +496,102 @@ bool launchable_columns(const Segments& s, int u) {
 
 }  // namespace
 
+namespace {
+
+// In how many shares a projection's sums are made (0: whole, in the larger tiles).
+// Below 16 steps a tile is short beside the launches (8 tokens of 4 experts, 1024 x
+// 512: 17 us whole, 25 in shares).  Up to one 128 x 128 tile for a compute unit the
+// shares give each unit one block (one expert of 2048 x 7168 whole and in shares, call
+// by call: one token 46 against 26 us, 64 tokens 54 against 32, 512 tokens 76 against
+// 66; twice the blocks 31, 41 and 69; 1021 tokens' up projections 62 us against 46 +
+// 6), and with a few rows an expert such tiles read the weights faster than the larger ones
+// (one token of 8 of 32 experts, up projections 53 us against 41 + 5).  There is no
+// second reason for one share of a down projection, whose tiles are as small.
+struct Shares {
+  int up, down;
+};
+Shares shares_of(int pairs, int E, int H, int I) {
+  const int busy = E < pairs ? E : pairs, rows = (pairs + busy - 1) / busy;
+  const auto shares = [&](int P, int K) {
+    const int64_t tiles =
+        (int64_t)busy * ((rows + NarrowCodes::kBv - 1) / NarrowCodes::kBv) * (P / NarrowCodes::kBu);
+    const int steps = K / kFp8Block;
+    if (steps < 16 || (tiles > kUnits && pairs / E > 4)) return 0;
+    const int64_t want = kUnits / tiles, most = steps / 2;
+    return (int)(want < 1 ? 1 : want < most ? want : most);
+  };
+  const int down = shares(H, I);
+  return {shares(2 * I, H), down > 1 ? down : 0};
+}
+
+size_t parts_bytes(size_t rows, Shares s, int H, int I) {
+  const size_t up = (size_t)s.up * 2 * I, down = (size_t)s.down * H;
+  return round_up(rows * (up > down ? up : down) * 4);
+}
+
+hipError_t launch_split(const SplitParams& p, int shares, hipStream_t st) {
+  using C = NarrowCodes;
+  constexpr int kLds = Fp8Product<C, kStages<C>>::kLds;
+  const hipError_t e = allow_lds<ffn_split_kernel<C>, kLds>();
+  if (e != hipSuccess) return e;
+  const int ntiles = p.P / C::kBu;
+  hipLaunchKernelGGL((ffn_split_kernel<C>),
+                     dim3((unsigned)tile_bound(p.seg, C::kBv, ntiles), shares), dim3(C::kThreads),
+                     kLds, st, p, ntiles);
+  return hipGetLastError();
+}
+
+// Blocks of a join: some 8 columns a thread once, if there are few rows.
+dim3 join_grid(const Segments& seg, int columns) {
+  const unsigned x = (unsigned)tile_bound(seg, kJoinRows, 1);
+  const unsigned most = (unsigned)(kJoinRows * columns / 8 + kJoinThreads - 1) / kJoinThreads;
+  return dim3(x, most < 16 ? most : 16);
+}
+
+}  // namespace
+
 size_t expert_ffn_workspace(int rows, int pairs, int E, int H, int I) {
   if (pairs == 0) return 0;
-  return round_up((size_t)rows * I) + round_up((size_t)rows * (I / kFp8Block) * 4);
+  const size_t n = rows;
+  return round_up(n * I) + round_up(n * (I / kFp8Block) * 4) +
+         parts_bytes(n, shares_of(pairs, E, H, I), H, I);
 }
 
 hipError_t launch_expert_ffn(const FfnParams& p, hipStream_t st) {
-  if (!launchable_columns(p.seg, p.I) || !launchable_columns(p.seg, p.H))
+  const Segments& seg = p.seg;
+  if (!launchable_columns(seg, 2 * p.I) || !launchable_columns(seg, p.H))
     return hipErrorNotSupported;
+  const Shares shares = shares_of(seg.pairs, seg.E, p.H, p.I);
+  const size_t n = seg.rows;
   Carver ws{static_cast<char*>(p.workspace)};
-  uint8_t* h = ws.take<uint8_t>((size_t)p.seg.rows * p.I);
-  float* h_scales = ws.take<float>((size_t)p.seg.rows * (p.I / kFp8Block));
-  const UpParams up{p.seg, p.x, p.x_scales, p.up, p.up_scales, p.pre, h, h_scales, p.H, p.I};
-  hipError_t e = large_codes(p.seg, 2 * p.I)
-                     ? launch_product<Codes, ffn_up_kernel<Codes>, kUpLds<Codes>>(up, p.I, 128, st)
-                     : launch_product<ShortCodes, ffn_up_kernel<ShortCodes>, kUpLds<ShortCodes>>(
-                           up, p.I, 128, st);
+  uint8_t* h = ws.take<uint8_t>(n * p.I);
+  float* h_scales = ws.take<float>(n * (p.I / kFp8Block));
+  float* parts = reinterpret_cast<float*>(ws.at);
+  const UpParams up{seg, p.x, p.x_scales, p.up, p.up_scales, p.pre, h, h_scales, p.H, p.I};
+  hipError_t e;
+  if (shares.up > 0) {
+    const SplitParams split{seg, p.x, p.x_scales, p.up, p.up_scales, parts, p.H, 2 * p.I};
+    e = launch_split(split, shares.up, st);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(ffn_join_up_kernel, join_grid(seg, p.I), dim3(kJoinThreads), 0, st, up,
+                       parts, shares.up);
+    e = hipGetLastError();
+  } else if (large_codes(seg, 2 * p.I)) {
+    e = launch_product<Codes, ffn_up_kernel<Codes>, kUpLds<Codes>>(up, p.I, 128, st);
+  } else {
+    e = launch_product<ShortCodes, ffn_up_kernel<ShortCodes>, kUpLds<ShortCodes>>(up, p.I, 128, st);
+  }
   if (e != hipSuccess) return e;
+  if (shares.down > 0) {
+    const SplitParams split{seg, h, h_scales, p.down, p.down_scales, parts, p.I, p.H};
+    e = launch_split(split, shares.down, st);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(ffn_join_down_kernel, join_grid(seg, p.H), dim3(kJoinThreads), 0, st, seg,
+                       parts, shares.down, p.residual, p.y, p.H);
+    return hipGetLastError();
+  }
   MatmulParams down{};
-  down.seg = p.seg;
+  down.seg = seg;
   down.x = h;
   down.x_scales = h_scales;
   down.weight = p.down;

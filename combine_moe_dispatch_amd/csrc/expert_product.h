@@ -419,12 +419,12 @@ struct Fp8Product {
   //
   // A wave multiplies row after row of fragments while it reads the next one, and
   // scales each product behind the second one after it.  B's fragments stay in
-  // registers for a step.  All waves meet twice a step: in front of the last row of
-  // A's first half, when that half, B and the scales are in registers and their
-  // place can be filled again, and in front of the last row, for the second half.
+  // registers for a step.  All waves meet twice a step: when A's first half, B and
+  // the scales are in registers and their place can be filled again, and when the
+  // second half is.
   // So a load has one and a half steps to arrive with two steps of LDS (with one
   // meeting a step, and one step to arrive, 4096 tokens' up projections took 955
-  // us, XXX now; without any wait for memory YYY).
+  // us, with two 918; without any wait for memory 850).
   template <int PART>
   __device__ __forceinline__ void run(char* smem, int wave, const char* bp, const float* scale,
                                       int blocks, int rows) {
@@ -523,26 +523,29 @@ struct Fp8Product {
     };
     constexpr int kProducts = C::kTu * PART, kBehind = 2, kSlots = kBehind + 1;
     static_assert(kBehind <= (C::kTu - 1) * PART, "a step's scales before the next one's");
-    i32x8_t fa[2], fb[PART];
+    // rows of A's fragments read ahead: one where a row is four products, else two
+    constexpr int kAhead = PART <= 2 ? 2 : 1, kRows = 2 * kAhead;
+    static_assert(C::kTu % kRows == 0 && kAhead <= kHalf, "the same places in every step");
+    i32x8_t fa[kRows], fb[PART];
     float sx[PART], sw[2], s[2][PART];
     f32x4_t part[kSlots];
     auto read_a = [&](int u) {
-      fa[u % 2] = frag(ra, here + u / kHalf * kSecondAt, u % kHalf);
+      fa[u % kRows] = frag(ra, here + u / kHalf * kSecondAt, u % kHalf);
     };
     auto read_b = [&](int v) {
       fb[v] = frag(rb, here + kRowsAt, v * C::kWv);
       sx[v] = lds_float(here + sx_at + v * C::kWv / 2 * 256);
     };
-    read_a(0);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) read_a(u);
 #pragma unroll
     for (int v = 0; v < PART; ++v) read_b(v);
     sw[0] = lds_float(here + sw_at);
     sw[1] = lds_float(here + sw_at + 4);
     // A first half's loads are started some with each row of products: all at once
     // they hold up the waves.
-    constexpr int kSpread = kHalf - 1 < 3 ? kHalf - 1 : 3;
+    constexpr int kSpread = kHalf < 3 ? kHalf : 3;  // all before the next meeting
     constexpr int kChunk = (kFirst + kSpread - 1) / kSpread;
-    static_assert(kSpread > 0 && kHalf % 2 == 0, "all before the next meeting, in two buffers");
     // LAST: no step follows.
     auto step = [&](int t, auto last) {
       constexpr bool kLast = decltype(last)::value;
@@ -553,26 +556,28 @@ struct Fp8Product {
         const int u = i / PART, v = i % PART;
         const bool row = i < kProducts && v == 0;
         if (row) {
-          if (u + 1 == kHalf) meet_first(t);
-          if (u + 1 < C::kTu) {
-            read_a(u + 1);
+          if (u + kAhead == kHalf) meet_first(t);
+          if (u + kAhead < C::kTu) {
+            read_a(u + kAhead);
           } else if (!kLast) {
-            meet_second(t);
-            here = after(here);
-            read_a(0);
+            if (u + kAhead == C::kTu) {
+              meet_second(t);
+              here = after(here);
+            }
+            read_a(u + kAhead - C::kTu);
           }
         }
         if (i < kProducts)
           part[i % kSlots] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              fa[u % 2], fb[v], f32x4_t{}, 0, 0, 0, 0, 0, 0);
+              fa[u % kRows], fb[v], f32x4_t{}, 0, 0, 0, 0, 0, 0);
         if (row && more) {
-          const int n = u + 1 - kHalf;
+          const int n = u + kAhead - kHalf;
           if (n >= 0 && n < kSpread) {
 #pragma unroll
             for (int q = 0; q < kChunk; ++q)
               if (n * kChunk + q < kFirst) load_first(n * kChunk + q, slot);
           }
-          if (u + 1 == C::kTu) start_second(slot);
+          if (u + kAhead == C::kTu) start_second(slot);
         }
         if (i >= kBehind) {
           const int j = i - kBehind, ju = j / PART, jv = j % PART;
