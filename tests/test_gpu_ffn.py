@@ -120,10 +120,10 @@ def check_untouched(case, t):
     assert (t.cpu()[~placed] == FILL).all(), "a row of no segment was written"
 
 
-def run_forward(case, residual=True):
+def run_forward(case, residual=True, most=40):
     r = case.bf16(case.ffn.hidden).cuda() if residual else None
     y, z = case.forward(r)
-    for e, rows in case.checked_rows():
+    for e, rows in case.checked_rows(most):
         if not rows:
             continue
         (wy, ty), (wz, tz) = plain.forward(case.x64[rows], case.up64[e], case.down64[e],
@@ -153,6 +153,26 @@ def test_forward(T, E, k, N, C, H, I):
 def test_forward_large_tiles(T, E, H, I):
     """Enough rows and columns for the largest tiles."""
     run_forward(Case(T, E, 1, 1, 0, H, I, seed=T))
+
+
+@pytest.mark.parametrize("T,E,k,N,C,H,I,dense", [
+    (1, 1, 1, 1, 0, 2048, 128, True),       # the first projection in shares: 8 of 16 steps
+    (5, 3, 2, 1, 0, 2176, 256, False),      # 17 steps
+    (130, 1, 1, 1, 0, 2048, 2048, True),    # both, and rows of a second tile
+    (40, 2, 1, 2, 64, 2048, 128, False),    # rows that nobody reaches
+    (300, 2, 1, 2, 100, 2304, 128, False),  # capacity overflows
+    (3, 40, 1, 1, 0, 2048, 256, False),     # a row an expert, most have none
+    (260, 1, 1, 1, 0, 128, 2176, True),     # the second projection alone
+])
+def test_sums_in_shares(T, E, k, N, C, H, I, dense):
+    case = Case(T, E, k, N, C, H, I, seed=T + H, dense=dense)
+    run_forward(case, residual=T % 2 == 1, most=10)
+    y, z = case.forward()
+    for _ in range(3):
+        a, b = case.forward()
+        assert torch.equal(a, y) and torch.equal(b, z)
+    again, _ = case.forward(pre=False)
+    assert torch.equal(again, y)
 
 
 @pytest.mark.parametrize("counts", [

@@ -262,6 +262,24 @@ def test_weights(E, P, K, dtype):
     assert (codes[-8:] == 0x55).all()
 
 
+@pytest.mark.parametrize("power", [-149, -148, -140, -126, -81, -80, 79, 80, 81, 100, 117])
+def test_weights_of_far_scales(power):
+    """Largest magnitudes from one smallest fp32 step to near the largest fp32 value,
+    where a scale is coarse or nothing, bit for bit."""
+    gen = torch.Generator().manual_seed(power + 200)
+    w = torch.randint(-600, 601, (128, 128), generator=gen).double() * 2.0 ** power
+    w[5, 7] = 600 * 2.0 ** power
+    w = w.float()
+    codes, scales = torch.empty(128, 128, dtype=torch.uint8, device="cuda"), torch.empty(1, device="cuda")
+    api.moe_quantize_weight(w.cuda(), codes, scales)
+    b = w.numpy()
+    s = np.abs(b).max() / np.float32(448)
+    q = b / s if s > 0 else np.zeros_like(b)
+    assert scales.item() == s
+    assert torch.equal(codes.cpu().view(torch.float8_e4m3fn).double(),
+                       plain.e4m3(torch.from_numpy(q.astype(np.float64))))
+
+
 def test_weights_with_a_nan():
     w = torch.ones(128, 256)
     w[7, 200] = float("nan")
