@@ -27,10 +27,21 @@ __device__ __forceinline__ void segment_of(const Segments& s, int e, int& begin,
   end = (int)min(last, (int64_t)s.rows);
 }
 
-// Eight neighbouring bf16 values to and from memory (16 bytes).
+// Eight neighbouring bf16 values to and from 16 bytes, and to and from memory.
+__device__ __forceinline__ void unpack8(float (&v)[8], uint4 q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  *reinterpret_cast<uint4*>(p) = pack8(v);
 }
 __device__ __forceinline__ void add8(float (&v)[8], const uint16_t* p) {
   const uint4 q = *reinterpret_cast<const uint4*>(p);

@@ -24,6 +24,8 @@ namespace {
 // three.  NarrowCodes: 128 by 128, two blocks to a compute unit.
 using ShortCodes = Config<2, 4, 8, 2>;
 using NarrowCodes = Config<2, 4, 4, 2>;
+// 256 by 64.
+using FlatCodes = Config<2, 4, 8, 1>;
 template <class C>
 constexpr int kStages = C::kTv == 4 || C::kTu == 4 ? 2 : 3;
 
@@ -255,8 +257,8 @@ ffn_join_down_kernel(Segments seg, const float* parts, int shares, const uint16_
 // Backward
 // ---------------------------------------------------------------------------
 // Placed rows of grad_y to 8 bits and of x to bf16 (code times scale, half a bf16
-// step off; NULL: not wanted): a stream, 16 rows a block.
-constexpr int kPrepareRows = 16, kPrepareThreads = 256;
+// step off; NULL: not wanted): a stream, 4 rows a block.
+constexpr int kPrepareRows = 4, kPrepareThreads = 256;
 
 struct PrepareParams {
   Segments seg;
@@ -330,61 +332,80 @@ struct SlopeParams {
 };
 
 // The slope of the activation on the accumulators; a wave has all 128 columns of a
-// scale block, of the gate's and of the up half's gradient.
+// scale block, of the gate's and of the up half's gradient.  A row's pre-activations
+// are loaded in front of the row's before it, whose stores they would else wait for.
 template <class C, class Product>
-__device__ __forceinline__ void finish_slope(const Product& prod, const SlopeParams& p,
-                                             const Tile& t, int wave) {
+__device__ __forceinline__ void finish_slope(Product& prod, const SlopeParams& p, const Tile& t,
+                                             int wave) {
   constexpr int kPairs = C::kTu / 2;
   static_assert(kPairs * 32 == kFp8Block, "a wave's columns are one block");
   const int wu = wave % C::kWu, wv = wave / C::kWu, lane = lane_id();
   const int col0 = (t.n * C::kWu + wu) * kFp8Block;
   if (col0 >= p.I) return;
   const int P = 2 * p.I, pb = P / kFp8Block;
+  const auto row_of = [&](int v) { return t.m0 + (v * C::kWv + wv) * 16 + (lane & 15); };
+  const auto column = [&](int a) { return t.n * C::kBu + Product::column(wu, a); };
+  struct Pre {
+    uint4 g[kPairs], u[kPairs];
+  };
+  const auto load = [&](Pre& q, int v) {
+    const uint16_t* pre = p.pre + (size_t)min(row_of(v), t.end - 1) * P;
+#pragma unroll
+    for (int a = 0; a < kPairs; ++a) {
+      q.g[a] = *reinterpret_cast<const uint4*>(pre + column(a));
+      q.u[a] = *reinterpret_cast<const uint4*>(pre + column(a) + p.I);
+    }
+  };
+  Pre here, next;
+  load(here, 0);
 #pragma unroll
   for (int v = 0; v < C::kTv; ++v) {
-    const int row = (v * C::kWv + wv) * 16 + (lane & 15), m = t.m0 + row;
+    if (v + 1 < C::kTv) load(next, v + 1);
+    const int m = row_of(v);
     const bool there = m < t.end;
-    const size_t at = (size_t)(there ? m : t.m0) * P;
-    float dg[kPairs][8], du[kPairs][8];
+    const size_t at = (size_t)m * P;
+    float du[kPairs][8];
     uint32_t largest_g = 0, largest_u = 0;
 #pragma unroll
     for (int a = 0; a < kPairs; ++a) {
-      const int col = t.n * C::kBu + Product::column(wu, a);
-      float gh[8], g[8], u[8], h[8];
-      prod.eight(gh, a, v);
-      load8(g, p.pre + at + col);
-      load8(u, p.pre + at + p.I + col);
+      float dg[8], g[8], u[8], h[8];
+      prod.eight(dg, a, v);
+      unpack8(g, here.g[a]);
+      unpack8(u, here.u[a]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = sigmoid_short(g[i]);
-        const float silu = g[i] * s;
-        dg[a][i] = gh[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
-        du[a][i] = gh[i] * silu;
+        const float s = sigmoid_short(g[i]), silu = g[i] * s;
+        du[a][i] = dg[i] * silu;
+        dg[i] = dg[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
         h[i] = silu * u[i];
-        largest_g = max(largest_g, magnitude(dg[a][i]));
+        largest_g = max(largest_g, magnitude(dg[i]));
         largest_u = max(largest_u, magnitude(du[a][i]));
+        prod.acc[2 * a + i / 4][v][i % 4] = dg[i];
       }
-      if (!there) continue;
-      if (p.h) store8(p.h + (size_t)m * p.I + col, h);
-      if (p.wide_gz) {
-        store8(p.wide_gz + at + col, dg[a]);
-        store8(p.wide_gz + at + p.I + col, du[a]);
+      if (there && p.h) store8(p.h + (size_t)m * p.I + column(a), h);
+      if (there && p.wide_gz) {
+        store8(p.wide_gz + at + column(a), dg);
+        store8(p.wide_gz + at + column(a) + p.I, du[a]);
       }
     }
-    if (!p.gz) continue;
-    const BlockScale gate(max_over_rows(largest_g)), up(max_over_rows(largest_u));
-    if (!there) continue;
+    if (p.gz) {
+      const BlockScale gate(max_over_rows(largest_g)), up(max_over_rows(largest_u));
+      if (there) {
 #pragma unroll
-    for (int a = 0; a < kPairs; ++a) {
-      const int col = t.n * C::kBu + Product::column(wu, a);
-      *reinterpret_cast<uint2*>(p.gz + at + col) = gate.codes(dg[a]);
-      *reinterpret_cast<uint2*>(p.gz + at + p.I + col) = up.codes(du[a]);
+        for (int a = 0; a < kPairs; ++a) {
+          float dg[8];
+          prod.eight(dg, a, v);
+          *reinterpret_cast<uint2*>(p.gz + at + column(a)) = gate.codes(dg);
+          *reinterpret_cast<uint2*>(p.gz + at + column(a) + p.I) = up.codes(du[a]);
+        }
+        if (lane < 16) {
+          float* scales = p.gz_scales + (size_t)m * pb + col0 / kFp8Block;
+          scales[0] = gate.scale;
+          scales[pb / 2] = up.scale;
+        }
+      }
     }
-    if (lane < 16) {
-      float* scales = p.gz_scales + (size_t)m * pb + col0 / kFp8Block;
-      scales[0] = gate.scale;
-      scales[pb / 2] = up.scale;
-    }
+    here = next;
   }
 }
 
@@ -473,6 +494,32 @@ hipError_t launch_product(const Params& p, int u, int cols, hipStream_t st) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(KERNEL, dim3((unsigned)grid), dim3(C::kThreads), LDS, st, p, ntiles);
   return hipGetLastError();
+}
+
+template <class C>
+struct SlopeKernel {
+  static constexpr auto kKernel = ffn_slope_kernel<C>;
+};
+template <class C>
+struct RowGradKernel {
+  static constexpr auto kKernel = ffn_grad_x_kernel<C>;
+};
+
+// A product with transposed weights, of u columns.  The shortest tiles while longer
+// ones would leave half the compute units idle: what a tile's rows take behind its
+// products counts as well (602 rows of 6 experts, 640 x 384: slopes 22 us on 12 tiles
+// of 128 rows, 14 on twice as many; the rows' gradient 10 against 8).
+template <template <class> class Kernel, class Params>
+hipError_t launch_transposed(const Params& p, int u, hipStream_t st) {
+  const auto launch = [&](auto config) {
+    using C = decltype(config);
+    constexpr int kLds = Fp8Product<C, kStages<C>, true>::kLds;
+    return launch_product<C, Kernel<C>::kKernel, kLds>(p, u, C::kBu, st);
+  };
+  if (large_codes(p.seg, u)) return launch(Codes{});
+  if (tiles_of(p.seg, u, ShortCodes::kBu, ShortCodes::kBv) <= kUnits / 2)
+    return launch(FlatCodes{});
+  return launch(ShortCodes{});
 }
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
@@ -645,17 +692,11 @@ hipError_t launch_expert_ffn_grad(const FfnGradParams& p, hipStream_t st) {
                             p.grad_x ? gz : nullptr, gz_scales,
                             p.grad_up ? wide_gz : nullptr, p.grad_down ? h : nullptr,
                             p.H,   p.I};
-    constexpr int kLds = Fp8Product<Codes, kStages<Codes>, true>::kLds;
-    constexpr int kFewLds = Fp8Product<ShortCodes, kStages<ShortCodes>, true>::kLds;
-    e = large_codes(seg, p.I)
-            ? launch_product<Codes, ffn_slope_kernel<Codes>, kLds>(slope, p.I, 256, st)
-            : launch_product<ShortCodes, ffn_slope_kernel<ShortCodes>, kFewLds>(slope, p.I, 256, st);
+    e = launch_transposed<SlopeKernel>(slope, p.I, st);
     if (e != hipSuccess) return e;
     if (p.grad_x) {
       const RowGradParams row{seg, gz, gz_scales, p.up, p.up_scales, p.grad_x, p.H, p.I};
-      e = large_codes(seg, p.H)
-              ? launch_product<Codes, ffn_grad_x_kernel<Codes>, kLds>(row, p.H, 256, st)
-              : launch_product<ShortCodes, ffn_grad_x_kernel<ShortCodes>, kFewLds>(row, p.H, 256, st);
+      e = launch_transposed<RowGradKernel>(row, p.H, st);
       if (e != hipSuccess) return e;
     }
   }

@@ -618,6 +618,8 @@ struct Fp8Product {
         run<C::kTv / 2>(smem, wave, bp, scale, blocks, rows);
       else
         run<C::kTv / 4>(smem, wave, bp, scale, blocks, rows);
+    } else if constexpr (C::kTv == 1) {
+      run<1>(smem, wave, bp, scale, blocks, rows);
     } else {
       static_assert(C::kTv % 2 == 0 && B::kLoads % 2 == 0, "whole loads of half a tile");
       if (rows > C::kBv / 2)
@@ -661,13 +663,7 @@ struct Fp8Product {
 };
 
 __device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
+  unpack8(v, *reinterpret_cast<const uint4*>(p));
 }
 
 // y (and pre): u runs over weight rows; a gated layer's wave takes half of its

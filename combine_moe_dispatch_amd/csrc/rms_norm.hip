@@ -38,19 +38,6 @@ struct BlockSum {
   }
 };
 
-__device__ __forceinline__ void unpack8(float (&v)[8], uint4 q) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
-
 // V vectors of 8 columns a thread, THREADS apart.
 template <int THREADS, int V>
 struct Row {

@@ -230,10 +230,11 @@ def test_backward(T, E, k, N, C, H, I):
     run_backward(Case(T, E, k, N, C, H, I, seed=T + 1))
 
 
-@pytest.mark.parametrize("T,E,H,I", [(700, 1, 128, 11136), (700, 1, 11136, 128)])
+@pytest.mark.parametrize("T,E,H,I", [(700, 1, 128, 11136), (700, 1, 11136, 128),
+                                     (1500, 1, 128, 11136), (1500, 1, 11136, 128)])
 def test_backward_large_tiles(T, E, H, I):
-    """Enough rows and columns for the largest tiles: of the activation's slope, of
-    the rows' gradient."""
+    """Enough rows and columns for the larger tiles and for the largest: of the
+    activation's slope, of the rows' gradient."""
     case = Case(T, E, 1, 1, 0, H, I, seed=T, dense=True)
     gy, pre = case.bf16(H, 0.01), case.bf16(2 * I)
     gx, gu, gd = case.backward(gy.cuda(), pre.cuda())
