@@ -484,10 +484,8 @@ using Large = Config<2, 2, 8, 8>;
 using Mid = Config<2, 2, 4, 4>;
 // 64 x 16 by four waves that share the steps.
 using Few = StreamProduct<4, 1, 4, 3>;
-// fp8, 256 token rows by 256 weight rows in two steps of LDS (Codes) or by 128 in
-// three: the large tile moves less per product (32 experts of 4096 x 7168: 512
-// rows each 444 us against 527, 128 rows 236 against 284), the small one has
-// twice the blocks and the deeper ring for few rows (64 rows 201 against 195).
+// fp8 where there are few large tiles: 256 token rows by 128 weight rows in three
+// steps of LDS.
 using FewCodes = Config<2, 4, 4, 4>;
 
 // Large tiles from 112 rows an expert on, where some experts begin to need two

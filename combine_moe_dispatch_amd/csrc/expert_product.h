@@ -727,11 +727,15 @@ inline int64_t tiles_of(const Segments& s, int u, int bu, int bv) {
   return busy * ((rows + bv - 1) / bv) * ((u + bu - 1) / bu);
 }
 
+// e4m3 in 256 x 256 tiles and two steps of LDS, where every compute unit gets one
+// and there are 16 rows an expert, so that most experts have some.  It moves less per
+// product than smaller tiles (32 experts of 4096 x 7168 against 128 x 256 tiles: 16
+// rows each 161 us against 164, 64 rows 169 against 187, 128 rows 196 against 234, 512
+// rows 499 against 624; one expert and 2048 rows, which make 128 tiles, with the way
+// back to 7168 columns 137 against 117).
 using Codes = Config<2, 4, 8, 4>;
-// The large fp8 tile where an expert has more than a quarter of its rows on
-// average and every compute unit gets one.
 inline bool large_codes(const Segments& s, int u) {
-  return s.pairs / s.E > Codes::kBv / 4 && tiles_of(s, u, Codes::kBu, Codes::kBv) >= kUnits;
+  return s.pairs / s.E >= 16 && tiles_of(s, u, Codes::kBu, Codes::kBv) >= kUnits;
 }
 
 // A launch has less than 2^32 threads.
