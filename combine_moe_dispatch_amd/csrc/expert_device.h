@@ -40,6 +40,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                     pack_bf16x2(v[6], v[7]));
 }
+__device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p) {
+  unpack8(v, *reinterpret_cast<const uint4*>(p));
+}
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = pack8(v);
 }

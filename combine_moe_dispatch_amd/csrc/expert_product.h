@@ -662,10 +662,6 @@ struct Fp8Product {
   }
 };
 
-__device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p) {
-  unpack8(v, *reinterpret_cast<const uint4*>(p));
-}
-
 // y (and pre): u runs over weight rows; a gated layer's wave takes half of its
 // fragments from the gate rows and half from the up rows of the same columns.
 template <class C, int ACT>

@@ -4,11 +4,13 @@
 //   t = bf16(x + residual), r = 1 / sqrt(mean t^2 + eps), v = t r w
 //   grad_x = r (a - n mean(a n)) + carried, a = g w, n = t r;  grad_w = sum g n
 //
-// A row stays in a block's registers between the sum over it and its results, so
-// every value is read and written once: both are streams.  A block takes row
-// after row with the next one's loads on their way, and keeps its columns'
-// weights.  The norm is of the rounded sum, which is what the next layer and the
-// backward pass see.
+// A row stays in registers (as it came, in bf16) between the sum over it and its
+// results, so every value is read and written once: both are streams (4096 rows of
+// 7168: 265 MB in 51 us, 5.2 TB/s; the gradient of 16384: 940 MB in 183 us, 5.1 TB/s).
+// L threads have a row, 16 to a whole block by its length, and take row after row,
+// the next one's loads on their way while this one is summed; they keep their
+// columns' weights.  The norm is of the rounded sum, which is what the next layer and
+// the backward pass see.
 #include "expert_device.h"
 #include "ffn.h"
 #include "quantize.h"
@@ -17,36 +19,47 @@ namespace moe {
 
 namespace {
 
-// Sum over a block; the two slots of one use are free again two uses later.
-template <int THREADS>
-struct BlockSum {
-  static constexpr int kWaves = THREADS / kWave;
-  float (*slots)[kWaves];  // [2] in LDS
+// L threads to a row, blocks of kThreads.
+template <int L>
+struct Group {
+  static constexpr int kThreads = L < 256 ? 256 : L;
+  static constexpr int kRows = kThreads / L;
+  static constexpr int kWaves = L > kWave ? L / kWave : 1;
+  float (*slots)[kWaves];  // [2] in LDS; one use's are free again two uses later
   int turn = 0;
 
-  __device__ __forceinline__ float operator()(float v) {
+  // (a whole block's row is the same number in all lanes, and its addresses scalar)
+  static __device__ __forceinline__ int lane() { return L >= 256 ? threadIdx.x : threadIdx.x % L; }
+  static __device__ __forceinline__ int64_t first() {
+    return L >= 256 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+  }
+  static __device__ __forceinline__ int64_t stride() { return (int64_t)gridDim.x * kRows; }
+  // A thread's vector i of 8 columns.
+  static __device__ __forceinline__ int column(int i) { return (lane() + i * L) * 8; }
+
+  __device__ __forceinline__ float sum(float v) {
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d);
+    for (int d = 1; d < (L < kWave ? L : kWave); d *= 2) v += __shfl_xor(v, d);
     if constexpr (kWaves == 1) return v;
     if (lane_id() == 0) slots[turn][threadIdx.x / kWave] = v;
     lds_barrier();
-    float sum = 0.0f;
+    float all = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) sum += slots[turn][w];
+    for (int w = 0; w < kWaves; ++w) all += slots[turn][w];
     turn ^= 1;
-    return sum;
+    return all;
   }
 };
 
-// V vectors of 8 columns a thread, THREADS apart.
-template <int THREADS, int V>
+// V vectors of 8 columns a thread.  A row that does not exist, or a null buffer, is
+// zeros.
+template <int L, int V>
 struct Row {
   uint4 q[V];
-  // A row that does not exist, or a null buffer, is zeros.
   __device__ __forceinline__ void load(const uint16_t* base, int64_t t, int T, int H) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * THREADS) * 8;
+      const int c = Group<L>::column(i);
       q[i] = make_uint4(0, 0, 0, 0);
       if (base && t < T && c < H)
         q[i] = *reinterpret_cast<const uint4*>(base + (size_t)t * H + c);
@@ -54,143 +67,209 @@ struct Row {
   }
 };
 
-template <int THREADS, int V>
-__device__ __forceinline__ void load_weights(float (&w)[V][8], const float* weight, int H) {
+// A thread's weights: kept, or (KEEP false) loaded for each use.
+template <int L, int V, bool KEEP>
+struct Weights {
+  float w[KEEP ? V : 1][8];
+  const float* base;
+  int H;
+  __device__ __forceinline__ void get(float (&v)[8], int i) const {
+    const int c = Group<L>::column(i);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (threadIdx.x + i * THREADS) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
-    if (c < H) add8(w[i], weight + c);
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (c < H) add8(v, base + c);
   }
-}
+  __device__ __forceinline__ Weights(const float* weight, int columns) : base(weight), H(columns) {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) get(w[i], i);
+    }
+  }
+  __device__ __forceinline__ void operator()(float (&v)[8], int i) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = w[i][j];
+    } else {
+      get(v, i);
+    }
+  }
+};
 
-template <int THREADS, int V>
-__global__ void __launch_bounds__(THREADS)
+// From 32 columns a thread of 1024 on nothing but the row itself fits the registers.
+template <int L, int V>
+constexpr bool kRoom = L < 1024 || V < 4;
+
+template <int L, int V>
+__global__ void __launch_bounds__(Group<L>::kThreads)
 rms_norm_kernel(NormParams p) {
-  __shared__ float s_slots[2][THREADS / kWave];
-  BlockSum<THREADS> block_sum{s_slots};
-  Row<THREADS, V> x, res;
-  int64_t t = blockIdx.x;
+  __shared__ float s_slots[2][Group<L>::kWaves];
+  Group<L> group{s_slots};
+  Row<L, V> x, res;
+  int64_t t = Group<L>::first();
   x.load(p.x, t, p.T, p.H);
   res.load(p.residual, t, p.T, p.H);
-  float w[V][8];
-  load_weights<THREADS, V>(w, p.weight, p.H);
-  for (; t < p.T; t += gridDim.x) {
-    float v[V][8];
+  const Weights<L, V, kRoom<L, V>> weights(p.weight, p.H);
+  for (; t < p.T; t += Group<L>::stride()) {
+    Row<L, V> total;
+    float wide[kRoom<L, V> ? V : 1][8];  // total in fp32
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      unpack8(v[i], x.q[i]);
+      float v[8];
+      unpack8(v, x.q[i]);
+      total.q[i] = x.q[i];
       if (p.residual) {
         float r[8];
         unpack8(r, res.q[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
-        x.q[i] = pack8(v[i]);
-        unpack8(v[i], x.q[i]);
+        for (int j = 0; j < 8; ++j) v[j] += r[j];
+        total.q[i] = pack8(v);
+        unpack8(v, total.q[i]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
-      const int c = (threadIdx.x + i * THREADS) * 8;
+      for (int j = 0; j < 8; ++j) {
+        sum = fmaf(v[j], v[j], sum);
+        if constexpr (kRoom<L, V>) wide[i][j] = v[j];
+      }
+      const int c = Group<L>::column(i);
       if (p.total && c < p.H)
-        *reinterpret_cast<uint4*>(p.total + (size_t)t * p.H + c) = x.q[i];
+        *reinterpret_cast<uint4*>(p.total + (size_t)t * p.H + c) = total.q[i];
     }
-    x.load(p.x, t + gridDim.x, p.T, p.H);
-    res.load(p.residual, t + gridDim.x, p.T, p.H);
-    const float r = 1.0f / sqrtf(block_sum(sum) / (float)p.H + p.eps);
-    if (p.inv_rms && threadIdx.x == 0) p.inv_rms[t] = r;
+    if constexpr (kRoom<L, V>) {
+      x.load(p.x, t + Group<L>::stride(), p.T, p.H);
+      res.load(p.residual, t + Group<L>::stride(), p.T, p.H);
+    }
+    const float r = 1.0f / sqrtf(group.sum(sum) / (float)p.H + p.eps);
+    if (p.inv_rms && Group<L>::lane() == 0) p.inv_rms[t] = r;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * THREADS) * 8;
+      const int c = Group<L>::column(i);
+      float w[8];
+      float (&v)[8] = wide[kRoom<L, V> ? i : 0];
+      if constexpr (!kRoom<L, V>) unpack8(v, total.q[i]);
+      weights(w, i);
       uint32_t largest = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[i][j] = v[i][j] * r * w[i][j];
-        largest = max(largest, magnitude(v[i][j]));
+        v[j] = v[j] * r * w[j];
+        largest = max(largest, magnitude(v[j]));
       }
       const size_t at = (size_t)t * p.H + c;
-      if (p.y && c < p.H) *reinterpret_cast<uint4*>(p.y + at) = pack8(v[i]);
+      if (p.y && c < p.H) *reinterpret_cast<uint4*>(p.y + at) = pack8(v);
       if (p.codes) {
         const BlockScale block(max_over_16(largest));  // 16 lanes: 128 columns
         if (c < p.H) {
-          *reinterpret_cast<uint2*>(p.codes + at) = block.codes(v[i]);
-          if (threadIdx.x % 16 == 0) p.scales[at / 128] = block.scale;
+          *reinterpret_cast<uint2*>(p.codes + at) = block.codes(v);
+          if (threadIdx.x % 16 == 0) p.scales[at / kFp8Block] = block.scale;
         }
       }
+    }
+    if constexpr (!kRoom<L, V>) {
+      x.load(p.x, t + Group<L>::stride(), p.T, p.H);
+      res.load(p.residual, t + Group<L>::stride(), p.T, p.H);
     }
   }
 }
 
-// parts: [gridDim.x][H] sums of this block's rows, or NULL.
-template <int THREADS, int V>
-__global__ void __launch_bounds__(THREADS)
+// parts: [gridDim.x * kRows][H] sums of each group's rows, or NULL.
+template <int L, int V>
+__global__ void __launch_bounds__(Group<L>::kThreads)
 rms_norm_grad_kernel(NormGradParams p, float* parts) {
-  __shared__ float s_slots[2][THREADS / kWave];
-  BlockSum<THREADS> block_sum{s_slots};
-  Row<THREADS, V> gy, total, carried;
-  int64_t t = blockIdx.x;
-  gy.load(p.grad_y, t, p.T, p.H);
-  total.load(p.total, t, p.T, p.H);
-  float r = t < p.T ? p.inv_rms[t] : 0.0f;
-  float w[V][8], gw[V][8] = {};
-  load_weights<THREADS, V>(w, p.weight, p.H);
-  for (; t < p.T; t += gridDim.x) {
-    carried.load(p.carried, t, p.T, p.H);
-    float a[V][8], n[V][8];
+  constexpr bool kHold = kRoom<L, V>;  // else a row is read again for its results
+  __shared__ float s_slots[2][Group<L>::kWaves];
+  Group<L> group{s_slots};
+  int64_t t = Group<L>::first();
+  Row<L, V> gy, total;
+  float r = 0.0f;
+  const auto load = [&](int64_t t) {
+    gy.load(p.grad_y, t, p.T, p.H);
+    total.load(p.total, t, p.T, p.H);
+    r = t < p.T ? p.inv_rms[t] : 0.0f;
+  };
+  load(t);
+  const Weights<L, V, kRoom<L, V>> weights(p.weight, p.H);
+  float gw[V][8] = {};
+  for (; t < p.T; t += Group<L>::stride()) {
+    const Row<L, V> gy_here = gy, total_here = total;
+    const float r_here = r;
+    Row<L, V> carried;
+    if constexpr (kHold) carried.load(p.carried, t, p.T, p.H);
+    if constexpr (kRoom<L, V>) load(t + Group<L>::stride());
+    // a = g w and n = t r of vector i
+    const auto values = [&](float (&g)[8], float (&n)[8], float (&a)[8], int i) {
+      float w[8];
+      unpack8(g, gy_here.q[i]);
+      unpack8(n, total_here.q[i]);
+      weights(w, i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        n[j] *= r_here;
+        a[j] = g[j] * w[j];
+      }
+    };
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      unpack8(a[i], gy.q[i]);
-      unpack8(n[i], total.q[i]);
+      float g[8], n[8], a[8];
+      values(g, n, a, i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        n[i][j] *= r;
-        gw[i][j] = fmaf(a[i][j], n[i][j], gw[i][j]);
-        a[i][j] *= w[i][j];
-        sum = fmaf(a[i][j], n[i][j], sum);
+        gw[i][j] = fmaf(g[j], n[j], gw[i][j]);
+        sum = fmaf(a[j], n[j], sum);
       }
     }
-    const int64_t next = t + gridDim.x;
-    gy.load(p.grad_y, next, p.T, p.H);
-    total.load(p.total, next, p.T, p.H);
-    const float r_next = next < p.T ? p.inv_rms[next] : 0.0f;
     if (p.grad_x) {
-      const float mean = block_sum(sum) / (float)p.H;
+      const float mean = group.sum(sum) / (float)p.H;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float c8[8];
-        unpack8(c8, carried.q[i]);
+        const int c = Group<L>::column(i);
+        if (c >= p.H) continue;
+        const size_t at = (size_t)t * p.H + c;
+        float g[8], n[8], a[8], more[8] = {};
+        if constexpr (kHold) {
+          values(g, n, a, i);
+          unpack8(more, carried.q[i]);
+        } else {
+          float w[8];
+          load8(g, p.grad_y + at);
+          load8(n, p.total + at);
+          weights(w, i);
+          if (p.carried) load8(more, p.carried + at);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[i][j] = fmaf(r, a[i][j] - n[i][j] * mean, c8[j]);
-        const int c = (threadIdx.x + i * THREADS) * 8;
-        if (c < p.H) *reinterpret_cast<uint4*>(p.grad_x + (size_t)t * p.H + c) = pack8(a[i]);
+          for (int j = 0; j < 8; ++j) {
+            n[j] *= r_here;
+            a[j] = g[j] * w[j];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = fmaf(r_here, a[j] - n[j] * mean, more[j]);
+        store8(p.grad_x + at, a);
       }
     }
-    r = r_next;
+    if constexpr (!kRoom<L, V>) load(t + Group<L>::stride());
   }
   if (!parts) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = (threadIdx.x + i * THREADS) * 8;
+    const int c = Group<L>::column(i);
     if (c >= p.H) continue;
-    float4* out = reinterpret_cast<float4*>(parts + (size_t)blockIdx.x * p.H + c);
+    float4* out = reinterpret_cast<float4*>(parts + (size_t)Group<L>::first() * p.H + c);
     out[0] = make_float4(gw[i][0], gw[i][1], gw[i][2], gw[i][3]);
     out[1] = make_float4(gw[i][4], gw[i][5], gw[i][6], gw[i][7]);
   }
 }
 
-// The blocks' sums, 64 columns a block: each of 16 waves adds every 16th part.
+// The groups' sums, 64 columns a block: each of 16 waves adds every 16th part.
 constexpr int kJoin = 16;
 __global__ void __launch_bounds__(kJoin * kWave)
-rms_norm_join_kernel(const float* parts, float* grad_weight, int blocks, int H) {
+rms_norm_join_kernel(const float* parts, float* grad_weight, int groups, int H) {
   __shared__ float s_sum[kJoin][kWave];
   const int lane = lane_id(), wave = threadIdx.x / kWave;
   const int c = blockIdx.x * kWave + lane;
   float sum = 0.0f;
   if (c < H) {
 #pragma unroll 8
-    for (int b = wave; b < blocks; b += kJoin) sum += parts[(size_t)b * H + c];
+    for (int g = wave; g < groups; g += kJoin) sum += parts[(size_t)g * H + c];
   }
   s_sum[wave][lane] = sum;
   __syncthreads();
@@ -200,64 +279,85 @@ rms_norm_join_kernel(const float* parts, float* grad_weight, int blocks, int H) 
   grad_weight[c] = sum;
 }
 
-constexpr int kNormBlocks = 1024;
-constexpr int kGradBlocks = 512;
+// Threads to a row and vectors a thread: narrow rows share a block (65536 rows of 256
+// columns, 256 threads each 97 us, 32 each 31 us; the gradient 154 against 42), and a
+// row has up to 32 columns a thread where there are many, so that several fit a compute
+// unit.
+struct Split {
+  int threads, vectors;
+};
+Split split_of(int T, int H) {
+  const int n = H / 8;  // vectors of a row
+  if (T > 1 && n <= 16) return {16, 1};
+  if (T > 1 && n <= 32) return {32, 1};
+  if (T > 1 && n <= 128) return {64, n <= 64 ? 1 : 2};
+  const int l = n <= 256 || (n <= 1024 && T > 256) ? 256 : 1024;
+  return {l, n <= l ? 1 : n <= 2 * l ? 2 : n <= 4 * l ? 4 : 8};
+}
 
-int blocks_of(int T, int most) { return T < 1 ? 1 : T < most ? T : most; }
+// Blocks of a launch: no more than so many, each with its rows.
+int blocks_of(int T, Split s, int most) {
+  const int rows = s.threads < 256 ? 256 / s.threads : 1;
+  const int blocks = (int)(((int64_t)T + rows - 1) / rows);
+  return blocks < 1 ? 1 : blocks < most ? blocks : most;
+}
+constexpr int kNormBlocks = 1024, kGradBlocks = 512;
+int groups_of(int T, int H) {
+  const Split s = split_of(T, H);
+  return blocks_of(T, s, kGradBlocks) * (s.threads < 256 ? 256 / s.threads : 1);
+}
 
-// Few rows: a block of 1024 threads each; else 256, which leave room for several
-// rows to a compute unit.
-bool wide_rows(int T, int H) { return H > 256 * 8 * 4 || T <= 256; }
+// call(L, V) as constants
+template <class Call>
+void with_split(Split s, const Call& call) {
+  const auto vectors = [&](auto l) {
+    using std::integral_constant;
+    if (s.vectors == 1) call(l, integral_constant<int, 1>{});
+    else if (s.vectors == 2) call(l, integral_constant<int, 2>{});
+    else if (s.vectors == 4) call(l, integral_constant<int, 4>{});
+    else if constexpr (decltype(l)::value == 1024) call(l, integral_constant<int, 8>{});
+  };
+  switch (s.threads) {
+    case 16: vectors(std::integral_constant<int, 16>{}); break;
+    case 32: vectors(std::integral_constant<int, 32>{}); break;
+    case 64: vectors(std::integral_constant<int, 64>{}); break;
+    case 256: vectors(std::integral_constant<int, 256>{}); break;
+    default: vectors(std::integral_constant<int, 1024>{}); break;
+  }
+}
 
 }  // namespace
 
 hipError_t launch_rms_norm(const NormParams& p, hipStream_t st) {
-  const dim3 grid(blocks_of(p.T, kNormBlocks));
-#define MOE_NORM(THREADS, V) \
-  hipLaunchKernelGGL((rms_norm_kernel<THREADS, V>), grid, dim3(THREADS), 0, st, p)
-  const int vectors = p.H / 8;
-  if (wide_rows(p.T, p.H)) {
-    if (vectors <= 1024) MOE_NORM(1024, 1);
-    else if (vectors <= 2048) MOE_NORM(1024, 2);
-    else if (vectors <= 4096) MOE_NORM(1024, 4);
-    else MOE_NORM(1024, 8);
-  } else {
-    if (vectors <= 256) MOE_NORM(256, 1);
-    else if (vectors <= 512) MOE_NORM(256, 2);
-    else MOE_NORM(256, 4);
-  }
-#undef MOE_NORM
+  const Split s = split_of(p.T, p.H);
+  const dim3 grid(blocks_of(p.T, s, kNormBlocks));
+  with_split(s, [&](auto l, auto v) {
+    constexpr int L = decltype(l)::value, V = decltype(v)::value;
+    hipLaunchKernelGGL((rms_norm_kernel<L, V>), grid, dim3(Group<L>::kThreads), 0, st, p);
+  });
   return hipGetLastError();
 }
 
 size_t rms_norm_grad_workspace(int T, int H) {
-  const int blocks = blocks_of(T, kGradBlocks);
-  return blocks > 1 ? (size_t)blocks * H * 4 : 0;
+  const int groups = groups_of(T, H);
+  return groups > 1 ? (size_t)groups * H * 4 : 0;
 }
 
 hipError_t launch_rms_norm_grad(const NormGradParams& p, hipStream_t st) {
-  const int blocks = blocks_of(p.T, kGradBlocks);
+  const Split s = split_of(p.T, p.H);
+  const int groups = groups_of(p.T, p.H);
   float* parts = !p.grad_weight ? nullptr
-                 : blocks > 1   ? static_cast<float*>(p.workspace)
+                 : groups > 1   ? static_cast<float*>(p.workspace)
                                 : p.grad_weight;
-  const dim3 grid(blocks);
-#define MOE_NORM_GRAD(THREADS, V) \
-  hipLaunchKernelGGL((rms_norm_grad_kernel<THREADS, V>), grid, dim3(THREADS), 0, st, p, parts)
-  const int vectors = p.H / 8;
-  if (wide_rows(p.T, p.H)) {
-    if (vectors <= 1024) MOE_NORM_GRAD(1024, 1);
-    else if (vectors <= 2048) MOE_NORM_GRAD(1024, 2);
-    else if (vectors <= 4096) MOE_NORM_GRAD(1024, 4);
-    else MOE_NORM_GRAD(1024, 8);
-  } else {
-    if (vectors <= 256) MOE_NORM_GRAD(256, 1);
-    else if (vectors <= 512) MOE_NORM_GRAD(256, 2);
-    else MOE_NORM_GRAD(256, 4);
-  }
-#undef MOE_NORM_GRAD
-  if (p.grad_weight && blocks > 1)
+  const dim3 grid(blocks_of(p.T, s, kGradBlocks));
+  with_split(s, [&](auto l, auto v) {
+    constexpr int L = decltype(l)::value, V = decltype(v)::value;
+    hipLaunchKernelGGL((rms_norm_grad_kernel<L, V>), grid, dim3(Group<L>::kThreads), 0, st, p,
+                       parts);
+  });
+  if (p.grad_weight && groups > 1)
     hipLaunchKernelGGL(rms_norm_join_kernel, dim3((p.H + kWave - 1) / kWave),
-                       dim3(kJoin * kWave), 0, st, parts, p.grad_weight, blocks, p.H);
+                       dim3(kJoin * kWave), 0, st, parts, p.grad_weight, groups, p.H);
   return hipGetLastError();
 }
 
