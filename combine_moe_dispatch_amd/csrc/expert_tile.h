@@ -216,7 +216,6 @@ struct OperandTile {
   // the rest is in the instructions' offsets.
   template <int N>
   struct Reader {
-    static constexpr bool kWhole = false;  // a step comes in kParts fragments
     static constexpr int kAts = !TRANSPOSED ? kParts : PAIRED ? N / 2 : N;
     uint32_t at[kAts];
     // apart: fragments of the operand between two of this reader's (transposed
