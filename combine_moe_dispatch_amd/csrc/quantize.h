@@ -51,7 +51,8 @@ struct BlockScale {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = v[i] * factor, q0 = x * inverse;
-      q[i] = fmaf(fmaf(-by, q0, x), inverse, q0);
+      // (this way round a remainder of 0 leaves a -0 its sign)
+      q[i] = fmaf(-fmaf(by, q0, -x), inverse, q0);
     }
     if (scale < 0x1p-126f) {
 #pragma unroll
@@ -63,7 +64,7 @@ struct BlockScale {
       const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
       c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], lo, true);
     }
-    return make_uint2(c[0], c[1]);
+    return scale == 0.0f ? make_uint2(0, 0) : make_uint2(c[0], c[1]);
   }
 };
 

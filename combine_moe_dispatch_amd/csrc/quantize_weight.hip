@@ -24,11 +24,7 @@ quantize_weight_kernel(const T* weight, int kb, uint8_t* codes, float* scales) {
   float v[kPasses][8];
   uint32_t largest = 0;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    add8(v[i], weight + at + i * kRows * K);
-  }
+  for (int i = 0; i < kPasses; ++i) load8(v[i], weight + at + i * kRows * K);
 #pragma unroll
   for (int i = 0; i < kPasses; ++i)
 #pragma unroll

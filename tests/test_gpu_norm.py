@@ -293,6 +293,31 @@ def test_weights_with_a_nan():
     assert (got[:, :128] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_signs_of_zeros(dtype):
+    """A -0 beside other values keeps its sign, as the division and its rounding would;
+    a block of zeros has codes of 0."""
+    w = torch.randn(128, 384, generator=torch.Generator().manual_seed(3)).to(dtype)
+    w[::3] = -0.0
+    w[1::3] = 0.0
+    w[:, 128:256] = -0.0
+    w[2, 256] = 1e9              # small ones round to zero
+    codes, scales = torch.empty(128, 384, dtype=torch.uint8, device="cuda"), torch.empty(3, device="cuda")
+    api.moe_quantize_weight(w.cuda(), codes, scales)
+    blocks = w.float().numpy().reshape(128, 3, 128)
+    s = np.abs(blocks).max((0, 2)) / np.float32(448)
+    with np.errstate(all="ignore"):
+        q = np.where(s[None, :, None] > 0, blocks / s[None, :, None], np.float32(0))
+    want = torch.from_numpy(q).to(torch.float8_e4m3fn).view(torch.uint8).view(128, 384)
+    assert torch.equal(codes.cpu(), want) and np.array_equal(scales.cpu().numpy(), s)
+    rows = w.bfloat16()
+    c, s = torch.empty(128, 384, dtype=torch.uint8, device="cuda"), torch.empty(128, 3, device="cuda")
+    api.moe_rms_norm(rows.cuda(), None, torch.ones(384, device="cuda"), EPS, None, None, c, s)
+    zeros = (rows == 0) & (s.cpu() > 0).repeat_interleave(128, 1)
+    assert torch.equal(c.cpu()[zeros] == 0x80, rows[zeros].signbit())
+    assert (c.cpu()[(s.cpu() == 0).repeat_interleave(128, 1)] == 0).all()
+
+
 def test_refusals_on_tensors():
     x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(256, device="cuda")
