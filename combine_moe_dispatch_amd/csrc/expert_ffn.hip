@@ -137,14 +137,30 @@ ffn_up_kernel(UpParams p, int ntiles) {
 // sums lie behind one another in fp32; a launch of its own adds them up and does
 // what comes after the product.  One token's way through one expert is its weights'
 // way from memory, and 32 tiles of 56 steps would leave that to 32 compute units.
+// The sums lie row behind placed row: a receive buffer of fixed capacity has room for
+// many more (128 tokens of 32 ranks of 4096: 131072 rows, of which 1024 are placed).
 // ---------------------------------------------------------------------------
+// Which of the placed rows the tile's first one is.
+__device__ __forceinline__ int placed_row(const Segments& s, const Tile& t) {
+  if (s.rows == s.pairs) return t.m0;  // any row will do
+  const int lane = lane_id();
+  int n = 0;
+  for (int base = 0; base <= t.e; base += kWave) {
+    if (base + lane > t.e) continue;
+    int begin, end;
+    segment_of(s, base + lane, begin, end);
+    n += base + lane == t.e ? t.m0 - begin : max(end - begin, 0);
+  }
+  return __builtin_amdgcn_readlane(wave_inclusive_sum_dpp(n), 63);
+}
+
 struct SplitParams {
   Segments seg;
   const uint8_t* x;
   const float* x_scales;
   const uint8_t* weight;
   const float* weight_scales;
-  float* parts;  // [gridDim.y][seg.rows][P]
+  float* parts;  // [gridDim.y][seg.pairs][P]
   int K, P;
 };
 
@@ -158,6 +174,7 @@ ffn_split_kernel(SplitParams p, int ntiles) {
   if (!find_tile<C::kBv>(p.seg, ntiles, blockIdx.x, t)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
   const int kb = p.K / kFp8Block, rows = min(C::kBv, t.end - t.m0);
+  const int placed = placed_row(p.seg, t);
   // every share has a step (the launch sees to that)
   const int first = (int)((int64_t)kb * blockIdx.y / gridDim.y);
   const int last = (int)((int64_t)kb * (blockIdx.y + 1) / gridDim.y);
@@ -178,9 +195,9 @@ ffn_split_kernel(SplitParams p, int ntiles) {
   const int wu = wave % C::kWu, wv = wave / C::kWu;
 #pragma unroll
   for (int v = 0; v < C::kTv; ++v) {
-    const int m = t.m0 + (v * C::kWv + wv) * 16 + (lane & 15);
-    if (m >= t.end) continue;
-    float* out = p.parts + ((size_t)blockIdx.y * p.seg.rows + m) * p.P + t.n * C::kBu;
+    const int row = (v * C::kWv + wv) * 16 + (lane & 15), at = placed + row;
+    if (row >= rows || at >= p.seg.pairs) continue;  // (whatever the counts say)
+    float* out = p.parts + ((size_t)blockIdx.y * p.seg.pairs + at) * p.P + t.n * C::kBu;
 #pragma unroll
     for (int a = 0; a < C::kTu / 2; ++a) {
       float o[8];
@@ -208,14 +225,15 @@ __global__ void __launch_bounds__(kJoinThreads)
 ffn_join_up_kernel(UpParams p, const float* parts, int shares) {
   Tile t;
   if (!find_tile<kJoinRows>(p.seg, 1, blockIdx.x, t)) return;
-  const int rows = min(kJoinRows, t.end - t.m0), units = p.I / 8;
-  const size_t apart = (size_t)p.seg.rows * (2 * p.I);
+  const int placed = placed_row(p.seg, t), units = p.I / 8;
+  const int rows = min(min(kJoinRows, t.end - t.m0), p.seg.pairs - placed);
+  const size_t apart = (size_t)p.seg.pairs * (2 * p.I);
   // units per row are a multiple of 16: the 16 lanes of a scale block stay together
   for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * units;
        i += gridDim.y * kJoinThreads) {
     const size_t m = t.m0 + i / units;
     const int c = i % units * 8;
-    const float* z = parts + m * (2 * p.I) + c;
+    const float* z = parts + ((size_t)placed + i / units) * (2 * p.I) + c;
     float g[8], u[8];
     add_shares(g, z, apart, shares);
     add_shares(u, z + p.I, apart, shares);
@@ -242,12 +260,13 @@ ffn_join_down_kernel(Segments seg, const float* parts, int shares, const uint16_
                      uint16_t* y, int H) {
   Tile t;
   if (!find_tile<kJoinRows>(seg, 1, blockIdx.x, t)) return;
-  const int rows = min(kJoinRows, t.end - t.m0), units = H / 8;
+  const int placed = placed_row(seg, t), units = H / 8;
+  const int rows = min(min(kJoinRows, t.end - t.m0), seg.pairs - placed);
   for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * units;
        i += gridDim.y * kJoinThreads) {
     const size_t at = (size_t)t.m0 * H + (size_t)i * 8;
     float v[8];
-    add_shares(v, parts + at, (size_t)seg.rows * H, shares);
+    add_shares(v, parts + (size_t)placed * H + (size_t)i * 8, (size_t)seg.pairs * H, shares);
     if (residual) add8(v, residual + at);
     store8(y + at, v);
   }
@@ -571,9 +590,9 @@ Shares shares_of(int pairs, int E, int H, int I) {
   return {shares(2 * I, H), down > 1 ? down : 0};
 }
 
-size_t parts_bytes(size_t rows, Shares s, int H, int I) {
+size_t parts_bytes(size_t pairs, Shares s, int H, int I) {
   const size_t up = (size_t)s.up * 2 * I, down = (size_t)s.down * H;
-  return round_up(rows * (up > down ? up : down) * 4);
+  return round_up(pairs * (up > down ? up : down) * 4);
 }
 
 hipError_t launch_split(const SplitParams& p, int shares, hipStream_t st) {
@@ -601,7 +620,7 @@ size_t expert_ffn_workspace(int rows, int pairs, int E, int H, int I) {
   if (pairs == 0) return 0;
   const size_t n = rows;
   return round_up(n * I) + round_up(n * (I / kFp8Block) * 4) +
-         parts_bytes(n, shares_of(pairs, E, H, I), H, I);
+         parts_bytes(pairs, shares_of(pairs, E, H, I), H, I);
 }
 
 hipError_t launch_expert_ffn(const FfnParams& p, hipStream_t st) {

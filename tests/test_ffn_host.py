@@ -162,6 +162,17 @@ def test_ffn_grad_refusals():
     assert ffn_grad(shape=(4, 128, 1024, 2, 2, 0, 1), f=(1 << 22, 128 * 1024)) == UNSUPPORTED
 
 
+def test_sums_in_shares_take_room_for_placed_rows_alone():
+    """128 tokens of 8 experts each have 1024 rows, wherever in 32 regions of 4096 they lie."""
+    H, I = 7168, 2048
+    ffn = api.Ffn(H, I)
+    packed = api.moe_expert_ffn_workspace_size(api.Shape(128, H, 256, 8, 32, 0, 1), ffn)
+    fixed = api.moe_expert_ffn_workspace_size(api.Shape(128, H, 256, 8, 32, 4096, 1), ffn)
+    row = I + I // 128 * 4    # the codes and scales between the projections
+    assert packed >= 1024 * (row + 2 * I * 4)
+    assert fixed - packed == (32 * 4096 - 1024) * row
+
+
 def test_binding_refuses_before_any_launch():
     cpu = torch.zeros(4, 256, dtype=torch.bfloat16)
     w = torch.ones(256)

@@ -160,6 +160,7 @@ def test_forward_large_tiles(T, E, H, I):
     (5, 3, 2, 1, 0, 2176, 256, False),      # 17 steps
     (130, 1, 1, 1, 0, 2048, 2048, True),    # both, and rows of a second tile
     (40, 2, 1, 2, 64, 2048, 128, False),    # rows that nobody reaches
+    (70, 80, 3, 8, 500, 2048, 2176, False), # sums lie by placed row: more than 64 experts
     (300, 2, 1, 2, 100, 2304, 128, False),  # capacity overflows
     (3, 40, 1, 1, 0, 2048, 256, False),     # a row an expert, most have none
     (260, 1, 1, 1, 0, 128, 2176, True),     # the second projection alone
