@@ -47,6 +47,7 @@ extern "C" {
  *                 (for a shared expert); both or neither; H % 128 == 0.
  *   inv_rms       [T] fp32 out, r (for the backward pass); or NULL.
  *   total, y may be x or residual themselves (not each other).
+ * Squares are summed in fp32: a row of values beyond 2^63 gives zeros.
  * At least one output.  H % 8 == 0; row buffers and weight are 16-byte aligned.
  * Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED for H > MOE_MAX_NORM_COLUMNS.
  */
@@ -158,7 +159,7 @@ size_t moe_expert_ffn_backward_workspace_size(const moe_shape *shape, const moe_
  *   workspace     moe_expert_ffn_backward_workspace_size bytes, 16-byte aligned, no
  *                 initialisation.
  * Errors as moe_expert_ffn; MOE_ERR_UNSUPPORTED also for weights of more than
- * 2^31 - 1 tiles of 128 x 128.
+ * 2^31 - 1 tiles of 128 x 128 and for more than some 2^26 rows.
  */
 moe_status moe_expert_ffn_backward(const moe_shape *shape, const moe_ffn *ffn, const void *grad_y,
                                    const void *x, const float *x_scales, const moe_layout *layout,
