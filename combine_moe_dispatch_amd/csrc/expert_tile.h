@@ -89,10 +89,10 @@ __device__ __forceinline__ void fill_table(int* begin, int* rows, const Segments
   }
 }
 
-// Most tiles a grouped product can have: every expert may end in a part tile.
+// Most tiles a grouped product can have: every expert may have one row in its last.
 inline int64_t tile_bound(const Segments& s, int bv, int ntiles) {
   const int64_t busy = s.E < s.pairs ? s.E : s.pairs;
-  return ((int64_t)s.pairs / bv + busy) * ntiles;
+  return ((s.pairs - busy) / bv + busy) * ntiles;
 }
 
 // 16 bytes a lane from base + offset to LDS, lane i at lds + 16 i.  The load
