@@ -23,7 +23,6 @@ namespace {
 // 256 columns of u by 256 token rows in two steps of LDS (Codes), or by 128 in
 // three.  NarrowCodes: 128 by 128, two blocks to a compute unit.
 using ShortCodes = Config<2, 4, 8, 2>;
-using NarrowCodes = Config<2, 4, 4, 2>;
 // 256 by 64.
 using FlatCodes = Config<2, 4, 8, 1>;
 template <class C>
@@ -574,30 +573,39 @@ bool launchable_columns(const Segments& s, int u) {
 
 namespace {
 
+// Tiles of u columns by C's rows, the rows evenly spread.
+template <class C>
+int64_t even_tiles(int pairs, int E, int u, int cols) {
+  const int busy = E < pairs ? E : pairs, rows = (pairs + busy - 1) / busy;
+  return (int64_t)busy * ((rows + C::kBv - 1) / C::kBv) * (u / cols);
+}
+
 // In how many shares a projection's sums are made (0: whole, in the larger tiles).
 // Below 16 steps a tile is short beside the launches (8 tokens of 4 experts, 1024 x
 // 512: 17 us whole, 25 in shares).  Up to one 128 x 128 tile for a compute unit the
 // shares give each unit one block (one expert of 2048 x 7168 whole and in shares, call
 // by call: one token 46 against 26 us, 64 tokens 54 against 32, 512 tokens 76 against
-// 66; twice the blocks 31, 41 and 69; 1021 tokens' up projections 62 us against 46 +
-// 6), and with a few rows an expert such tiles read the weights faster than the larger ones
-// (one token of 8 of 32 experts, up projections 53 us against 41 + 5).  There is no
-// second reason for one share of a down projection, whose tiles are as small.
+// 46; twice the blocks 31, 41 and 69), and with a few rows an expert such tiles read
+// the weights faster than the larger ones (one token of 8 of 32 experts, up projections
+// 53 us against 41 + 5).  There is no second reason for one share of a down projection,
+// whose tiles are as small, nor of the up projections where tiles of 256 x 64 are as
+// many (1021 tokens of one expert 74 us against 69, 600 tokens 63 against 60; but one
+// token of 8 experts, which makes half as many, 68 against 80).
 struct Shares {
   int up, down;
 };
 Shares shares_of(int pairs, int E, int H, int I) {
-  const int busy = E < pairs ? E : pairs, rows = (pairs + busy - 1) / busy;
   const auto shares = [&](int P, int K) {
-    const int64_t tiles =
-        (int64_t)busy * ((rows + NarrowCodes::kBv - 1) / NarrowCodes::kBv) * (P / NarrowCodes::kBu);
+    const int64_t tiles = even_tiles<NarrowCodes>(pairs, E, P, NarrowCodes::kBu);
     const int steps = K / kFp8Block;
     if (steps < 16 || (tiles > kUnits && pairs / E > 4)) return 0;
     const int64_t want = kUnits / tiles, most = steps / 2;
     return (int)(want < 1 ? 1 : want < most ? want : most);
   };
-  const int down = shares(H, I);
-  return {shares(2 * I, H), down > 1 ? down : 0};
+  const int up = shares(2 * I, H), down = shares(H, I);
+  const int64_t flat = even_tiles<FlatCodes>(pairs, E, I, kFp8Block);
+  const bool whole = up == 1 && flat > kUnits / 2 && flat <= kUnits;
+  return {whole ? 0 : up, down > 1 ? down : 0};
 }
 
 size_t parts_bytes(size_t pairs, Shares s, int H, int I) {
@@ -652,6 +660,8 @@ hipError_t launch_expert_ffn(const FfnParams& p, hipStream_t st) {
     hipLaunchKernelGGL(ffn_join_up_kernel, join_grid(seg, p.I), dim3(kJoinThreads), 0, st, up,
                        parts, shares.up);
     e = hipGetLastError();
+  } else if (even_tiles<FlatCodes>(seg.pairs, seg.E, p.I, kFp8Block) <= kUnits) {
+    e = launch_product<FlatCodes, ffn_up_kernel<FlatCodes>, kUpLds<FlatCodes>>(up, p.I, 128, st);
   } else if (large_codes(seg, 2 * p.I)) {
     e = launch_product<Codes, ffn_up_kernel<Codes>, kUpLds<Codes>>(up, p.I, 128, st);
   } else {

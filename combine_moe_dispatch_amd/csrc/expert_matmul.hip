@@ -484,8 +484,12 @@ using Large = Config<2, 2, 8, 8>;
 using Mid = Config<2, 2, 4, 4>;
 // 64 x 16 by four waves that share the steps.
 using Few = StreamProduct<4, 1, 4, 3>;
-// fp8 where there are few large tiles: 256 token rows by 128 weight rows in three
-// steps of LDS.
+// fp8 where there are few large tiles and more than 128 rows an expert: 256 token rows
+// by 128 weight rows in three steps of LDS, unless 128 x 128 tiles find a compute unit
+// each (4096 x 7168, one expert: 200 rows 52 us against 35, 1021 rows 55 against 41,
+// 1500 rows 59 against 68; 8 experts of 130 rows 56 against 80).  With up to 128 rows
+// there are as many of these, two to a unit (32 experts of 8 rows 159 us against 157;
+// 16 rows and 2048 x 7168, 24.5 us against 22).
 using FewCodes = Config<2, 4, 4, 4>;
 
 // Large tiles from 112 rows an expert on, where some experts begin to need two
@@ -569,6 +573,9 @@ template <int ACT>
 hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
   if (fp8) {
     if (large_codes(p.seg, p.P)) return launch_codes<Codes, 2, ACT>(p, st);
+    if (p.seg.pairs / p.seg.E <= 128 ||
+        tiles_of(p.seg, p.P, NarrowCodes::kBu, NarrowCodes::kBv) <= kUnits)
+      return launch_codes<NarrowCodes, 2, ACT>(p, st);
     return launch_codes<FewCodes, 3, ACT>(p, st);
   }
   if (large_tiles(p.seg, p.P)) return launch_tiles<Large, ACT>(p, st);

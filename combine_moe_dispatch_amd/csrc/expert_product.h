@@ -764,6 +764,8 @@ inline int64_t tiles_of(const Segments& s, int u, int bu, int bv) {
 // rows 499 against 624; one expert and 2048 rows, which make 128 tiles, with the way
 // back to 7168 columns 137 against 117).
 using Codes = Config<2, 4, 8, 4>;
+// 128 x 128, two blocks to a compute unit.
+using NarrowCodes = Config<2, 4, 4, 2>;
 inline bool large_codes(const Segments& s, int u) {
   return s.pairs / s.E >= 16 && tiles_of(s, u, Codes::kBu, Codes::kBv) >= kUnits;
 }
