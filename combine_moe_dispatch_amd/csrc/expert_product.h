@@ -437,15 +437,6 @@ struct Fp8Product {
     return f.v;
   }
 
-  // Wait for all loads but those of the last steps, at most MOST, and MORE.
-  template <int MOST, int LOADS, int MORE>
-  static __device__ __forceinline__ void wait_but(int steps) {
-    if constexpr (MOST > 0) {
-      if (steps < MOST) return wait_but<MOST - 1, LOADS, MORE>(steps);
-    }
-    wait_vm<MOST * LOADS + MORE>();
-  }
-
   // PART: as in TileProduct.  blocks > 0 steps.  scale: the scale this lane brings
   // in, of step 0: lanes 0-31 one of the wave's 32 x rows, lanes 32 and 33 those of
   // the weight rows behind the first and the second half of the wave's fragments.
@@ -507,14 +498,20 @@ struct Fp8Product {
       here = after(here);
     }
     here = lds;
-    wait_but<STAGES - 1, kLoads, kSecond>(blocks - 1);
+    if (blocks >= STAGES)
+      wait_vm<(STAGES - 1) * kLoads + kSecond>();
+    else
+      wait_vm<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     // All waves have read the first half, B and the scales of step t out, and its
     // second half has come.
     auto meet_first = [&](int t) {
       wait_lds();
-      wait_but<STAGES - 1, kLoads, 0>(blocks - 1 - t);
+      if (t + STAGES <= blocks)
+        wait_vm<(STAGES - 1) * kLoads>();
+      else
+        wait_vm<0>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     };
@@ -523,8 +520,10 @@ struct Fp8Product {
       wait_lds();
       if (t + STAGES < blocks)
         wait_vm<(STAGES - 1) * kLoads>();
+      else if (t + STAGES == blocks)
+        wait_vm<(STAGES - 2) * kLoads + kSecond>();
       else
-        wait_but<STAGES - 2, kLoads, kSecond>(blocks - 2 - t);
+        wait_vm<0>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     };
