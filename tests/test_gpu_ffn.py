@@ -155,6 +155,15 @@ def test_forward_large_tiles(T, E, H, I):
     run_forward(Case(T, E, 1, 1, 0, H, I, seed=T))
 
 
+@pytest.mark.parametrize("T,E,H,I", [
+    (1000, 1, 2048, 2048),    # 256 tiles of 64 rows: whole, one to a compute unit
+    (600, 1, 2176, 1792),     # 140 of them
+    (1100, 2, 256, 2176),     # 306: tiles of 128 rows
+])
+def test_forward_flat_tiles(T, E, H, I):
+    run_forward(Case(T, E, 1, 1, 0, H, I, seed=T), most=20)
+
+
 @pytest.mark.parametrize("T,E,k,N,C,H,I,dense", [
     (1, 1, 1, 1, 0, 2048, 128, True),       # the first projection in shares: 8 of 16 steps
     (5, 3, 2, 1, 0, 2176, 256, False),      # 17 steps
