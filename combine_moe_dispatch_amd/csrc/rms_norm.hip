@@ -171,7 +171,13 @@ rms_norm_kernel(NormParams p) {
   }
 }
 
-// parts: [gridDim.x * kRows][H] sums of each group's rows, or NULL.
+__device__ __forceinline__ void store_sums(float* out, const float (&v)[8]) {
+  reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// parts: [gridDim.x * kRows][H] sums of each group's rows, or NULL.  Where the row
+// itself fills the registers they are rms_norm_columns_kernel's.
 template <int L, int V>
 __global__ void __launch_bounds__(Group<L>::kThreads)
 rms_norm_grad_kernel(NormGradParams p, float* parts) {
@@ -188,7 +194,7 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
   };
   load(t);
   const Weights<L, V, kRoom<L, V>> weights(p.weight, p.H);
-  float gw[V][8] = {};
+  float gw[kHold ? V : 1][8] = {};
   for (; t < p.T; t += Group<L>::stride()) {
     const Row<L, V> gy_here = gy, total_here = total;
     const float r_here = r;
@@ -214,7 +220,7 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
       values(g, n, a, i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        gw[i][j] = fmaf(g[j], n[j], gw[i][j]);
+        if constexpr (kHold) gw[i][j] = fmaf(g[j], n[j], gw[i][j]);
         sum = fmaf(a[j], n[j], sum);
       }
     }
@@ -248,15 +254,36 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
     }
     if constexpr (!kRoom<L, V>) load(t + Group<L>::stride());
   }
-  if (!parts) return;
+  if constexpr (kHold) {
+    if (!parts) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = Group<L>::column(i);
-    if (c >= p.H) continue;
-    float4* out = reinterpret_cast<float4*>(parts + (size_t)Group<L>::first() * p.H + c);
-    out[0] = make_float4(gw[i][0], gw[i][1], gw[i][2], gw[i][3]);
-    out[1] = make_float4(gw[i][4], gw[i][5], gw[i][6], gw[i][7]);
+    for (int i = 0; i < V; ++i) {
+      const int c = Group<L>::column(i);
+      if (c < p.H) store_sums(parts + (size_t)Group<L>::first() * p.H + c, gw[i]);
+    }
   }
+}
+
+// Sums over rows of grad_y n for rows of more columns than a block can keep: 2048
+// columns a block, rows blockIdx.y, + gridDim.y, ..  It reads both operands a second
+// time, where the sums beside the row would spill (TIMES).
+constexpr int kWideThreads = 256, kWideGroups = 64;
+__global__ void __launch_bounds__(kWideThreads)
+rms_norm_columns_kernel(NormGradParams p, float* parts) {
+  const int c = (blockIdx.x * kWideThreads + threadIdx.x) * 8;
+  if (c >= p.H) return;
+  float gw[8] = {};
+#pragma unroll 4
+  for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
+    const size_t at = (size_t)t * p.H + c;
+    const float r = p.inv_rms[t];
+    float g[8], n[8];
+    load8(g, p.grad_y + at);
+    load8(n, p.total + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[j] = fmaf(g[j], n[j] * r, gw[j]);
+  }
+  store_sums(parts + (size_t)blockIdx.y * p.H + c, gw);
 }
 
 // The groups' sums, 64 columns a block: each of 16 waves adds every 16th part.
@@ -302,8 +329,10 @@ int blocks_of(int T, Split s, int most) {
   return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 constexpr int kNormBlocks = 1024, kGradBlocks = 512;
+bool wide(Split s) { return s.threads == 1024 && s.vectors >= 4; }  // as kRoom
 int groups_of(int T, int H) {
   const Split s = split_of(T, H);
+  if (wide(s)) return T < 1 ? 1 : T < kWideGroups ? T : kWideGroups;
   return blocks_of(T, s, kGradBlocks) * (s.threads < 256 ? 256 / s.threads : 1);
 }
 
@@ -350,11 +379,16 @@ hipError_t launch_rms_norm_grad(const NormGradParams& p, hipStream_t st) {
                  : groups > 1   ? static_cast<float*>(p.workspace)
                                 : p.grad_weight;
   const dim3 grid(blocks_of(p.T, s, kGradBlocks));
-  with_split(s, [&](auto l, auto v) {
-    constexpr int L = decltype(l)::value, V = decltype(v)::value;
-    hipLaunchKernelGGL((rms_norm_grad_kernel<L, V>), grid, dim3(Group<L>::kThreads), 0, st, p,
-                       parts);
-  });
+  if (parts && wide(s))
+    hipLaunchKernelGGL(rms_norm_columns_kernel,
+                       dim3((p.H / 8 + kWideThreads - 1) / kWideThreads, groups),
+                       dim3(kWideThreads), 0, st, p, parts);
+  if (p.grad_x || !wide(s))
+    with_split(s, [&](auto l, auto v) {
+      constexpr int L = decltype(l)::value, V = decltype(v)::value;
+      hipLaunchKernelGGL((rms_norm_grad_kernel<L, V>), grid, dim3(Group<L>::kThreads), 0, st, p,
+                         parts);
+    });
   if (p.grad_weight && groups > 1)
     hipLaunchKernelGGL(rms_norm_join_kernel, dim3((p.H + kWave - 1) / kWave),
                        dim3(kJoin * kWave), 0, st, parts, p.grad_weight, groups, p.H);

@@ -181,6 +181,25 @@ def test_norm_gradient_of_some(kw):
     grads(900, 640, **kw)
 
 
+@pytest.mark.parametrize("T,H,kw", [(150, 16392, {}), (65, 40960, dict(carried=False)), (64, 65536, {}),
+                                    (70, 32776, dict(gx=False)), (70, 16392, dict(gw=False)),
+                                    (1, 20000, dict(gx=False))])
+def test_norm_gradient_of_wide_rows(T, H, kw):
+    grads(T, H, seed=T, **kw)
+
+
+@pytest.mark.parametrize("T,H", [(0, 32768), (90, 32768)])
+def test_norm_gradient_of_wide_rows_in_place(T, H):
+    t, w = rows(T, H, 3).cuda(), norm_weight(H, 3).cuda()
+    gy = rows(T, H, 4).cuda()
+    r = (t.double().square().mean(1) + EPS).rsqrt().float()
+    gx, gw, again = torch.empty_like(t), torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    api.moe_rms_norm_backward(gy, t, w, r, None, gx, gw)
+    api.moe_rms_norm_backward(gy, t, w, r, None, gy, again)
+    assert torch.equal(gy, gx) and torch.equal(again, gw)
+    assert T > 0 or (gw == 0).all()
+
+
 def test_norm_gradient_without_rows():
     w = torch.ones(64, device="cuda")
     gw = torch.full((64,), FILL, device="cuda")
