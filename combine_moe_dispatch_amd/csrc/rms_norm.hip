@@ -181,7 +181,8 @@ __device__ __forceinline__ void store_sums(float* out, const float (&v)[8]) {
 template <int L, int V>
 __global__ void __launch_bounds__(Group<L>::kThreads)
 rms_norm_grad_kernel(NormGradParams p, float* parts) {
-  constexpr bool kHold = kRoom<L, V>;  // else a row is read again for its results
+  // else a row is read again for its results (1024 rows of 65536 278 us against 256)
+  constexpr bool kHold = V < 8;
   __shared__ float s_slots[2][Group<L>::kWaves];
   Group<L> group{s_slots};
   int64_t t = Group<L>::first();
@@ -194,12 +195,12 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
   };
   load(t);
   const Weights<L, V, kRoom<L, V>> weights(p.weight, p.H);
-  float gw[kHold ? V : 1][8] = {};
+  float gw[kRoom<L, V> ? V : 1][8] = {};
   for (; t < p.T; t += Group<L>::stride()) {
     const Row<L, V> gy_here = gy, total_here = total;
     const float r_here = r;
-    Row<L, V> carried;
-    if constexpr (kHold) carried.load(p.carried, t, p.T, p.H);
+    Row<L, kRoom<L, V> ? V : 1> carried;
+    if constexpr (kRoom<L, V>) carried.load(p.carried, t, p.T, p.H);
     if constexpr (kRoom<L, V>) load(t + Group<L>::stride());
     // a = g w and n = t r of vector i
     const auto values = [&](float (&g)[8], float (&n)[8], float (&a)[8], int i) {
@@ -220,7 +221,7 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
       values(g, n, a, i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if constexpr (kHold) gw[i][j] = fmaf(g[j], n[j], gw[i][j]);
+        if constexpr (kRoom<L, V>) gw[i][j] = fmaf(g[j], n[j], gw[i][j]);
         sum = fmaf(a[j], n[j], sum);
       }
     }
@@ -234,19 +235,21 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
         float g[8], n[8], a[8], more[8] = {};
         if constexpr (kHold) {
           values(g, n, a, i);
-          unpack8(more, carried.q[i]);
         } else {
           float w[8];
           load8(g, p.grad_y + at);
           load8(n, p.total + at);
           weights(w, i);
-          if (p.carried) load8(more, p.carried + at);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             n[j] *= r_here;
             a[j] = g[j] * w[j];
           }
         }
+        if constexpr (kRoom<L, V>)
+          unpack8(more, carried.q[i]);
+        else if (p.carried)
+          load8(more, p.carried + at);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = fmaf(r_here, a[j] - n[j] * mean, more[j]);
         store8(p.grad_x + at, a);
@@ -254,7 +257,7 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
     }
     if constexpr (!kRoom<L, V>) load(t + Group<L>::stride());
   }
-  if constexpr (kHold) {
+  if constexpr (kRoom<L, V>) {
     if (!parts) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -266,7 +269,8 @@ rms_norm_grad_kernel(NormGradParams p, float* parts) {
 
 // Sums over rows of grad_y n for rows of more columns than a block can keep: 2048
 // columns a block, rows blockIdx.y, + gridDim.y, ..  It reads both operands a second
-// time, where the sums beside the row would spill (TIMES).
+// time, where the sums beside the row would spill (2048
+// rows of 32768 248 us, so 174; 1024 of 65536 737 and 256).
 constexpr int kWideThreads = 256, kWideGroups = 64;
 __global__ void __launch_bounds__(kWideThreads)
 rms_norm_columns_kernel(NormGradParams p, float* parts) {
