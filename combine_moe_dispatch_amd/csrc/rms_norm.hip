@@ -95,6 +95,9 @@ struct Weights {
   }
 };
 
+// A mean of squares from here on has lost none that count: those below 2^-126.
+constexpr float kLeastMean = 0x1p-100f;
+
 // From 32 columns a thread of 1024 on nothing but the row itself fits the registers.
 template <int L, int V>
 constexpr bool kRoom = L < 1024 || V < 4;
@@ -139,7 +142,24 @@ rms_norm_kernel(NormParams p) {
       x.load(p.x, t + Group<L>::stride(), p.T, p.H);
       res.load(p.residual, t + Group<L>::stride(), p.T, p.H);
     }
-    const float r = 1.0f / sqrtf(group.sum(sum) / (float)p.H + p.eps);
+    const float mean = group.sum(sum) / (float)p.H + p.eps;
+    float r = 1.0f / sqrtf(mean);
+    if (mean < kLeastMean || mean == __builtin_inff()) {
+      // squares past the range of fp32: those of the values times a power of two
+      const float by = mean < 1.0f ? 0x1p80f : 0x1p-80f;
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float v[8];
+        if constexpr (!kRoom<L, V>) unpack8(v, total.q[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float scaled = (kRoom<L, V> ? wide[kRoom<L, V> ? i : 0][j] : v[j]) * by;
+          sum = fmaf(scaled, scaled, sum);
+        }
+      }
+      r = by / sqrtf(group.sum(sum) / (float)p.H + p.eps * by * by);
+    }
     if (p.inv_rms && Group<L>::lane() == 0) p.inv_rms[t] = r;
 #pragma unroll
     for (int i = 0; i < V; ++i) {

@@ -47,7 +47,9 @@ extern "C" {
  *                 (for a shared expert); both or neither; H % 128 == 0.
  *   inv_rms       [T] fp32 out, r (for the backward pass); or NULL.
  *   total, y may be x or residual themselves (not each other).
- * Squares are summed in fp32: a row of values beyond 2^63 gives zeros.
+ * Squares are summed in fp32, where they leave its range those of the row times
+ * 2^80 or 2^-80: any finite row will do.  Without eps a row of zeros, or of less than
+ * 2^-127, has no r in fp32.
  * At least one output.  H % 8 == 0; row buffers and weight are 16-byte aligned.
  * Errors: MOE_ERR_INVALID_ARG; MOE_ERR_UNSUPPORTED for H > MOE_MAX_NORM_COLUMNS.
  */

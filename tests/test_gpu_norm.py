@@ -377,3 +377,38 @@ def test_rows_past_2_31_elements():
     want_x, want_w = plain.norm_grad(t, t, w.double(), inv[at].double().cpu(), None)
     check(gx[at], *want_x, "grad_x")
     check(gw, want_w[0], want_w[1], "grad_weight")   # the other rows are zeros
+
+
+# Thread layouts: a row to 16, 32, 64, 256 and 1024 threads, to kept and to reloaded rows.
+LAYOUTS = [(1, 128), (60, 128), (60, 256), (60, 512), (60, 1024), (60, 2048), (300, 4096),
+           (300, 8192), (60, 8320), (3, 16384), (60, 16512), (20, 32896), (20, 65536)]
+
+
+@pytest.mark.parametrize("T,H", LAYOUTS)
+@pytest.mark.parametrize("eps", [EPS, 0.0])
+def test_norm_of_rows_whose_squares_leave_fp32(T, H, eps):
+    """Rows of any finite values that bf16 holds: squares from 2^-240 to 2^252, one value
+    among small ones, and the same through the gradient."""
+    powers = [124, 120, 70, 64, 63, 60, 56, 20, -60, -70, -110, -120]
+    gen = torch.Generator().manual_seed(T + H)
+    x = torch.randn(T, H, generator=gen, dtype=torch.float64)
+    x *= torch.tensor([2.0 ** powers[i % len(powers)] for i in range(T)]).double()[:, None]
+    if T > 20:
+        x[13], x[14] = x[13].sign(), x[14].sign()
+        x[13, H // 2], x[14, 3] = 2.0 ** 100, -2.0 ** 118
+        x[15], x[16] = -2.0 ** 127, 2.0 ** 64 / H ** 0.5
+    x, w = x.bfloat16(), norm_weight(H, T)
+    assert x.isfinite().all()
+    y, c, s = out(T, H), out(T, H, torch.uint8), out(T, H // 128, torch.float32)
+    inv = torch.full((T + 1,), FILL, device="cuda")
+    api.moe_rms_norm(x.cuda(), None, w.cuda(), eps, None, y, c, s, inv)
+    v, dv, r, dr = plain.norm(x.double(), w.double(), eps)
+    check(inv[:T], r, dr, "1 / rms")
+    check(y[:T], v, plain.rounded16(v, dv), "y")
+    check_codes(c[:T], s[:T], v, dv)
+    gy = (0.01 * torch.randn(T, H, generator=gen)).bfloat16()
+    gx, gw = out(T, H), torch.empty(H, device="cuda")
+    api.moe_rms_norm_backward(gy.cuda(), x.cuda(), w.cuda(), inv[:T], None, gx, gw)
+    want_x, want_w = plain.norm_grad(gy.double(), x.double(), w.double(), inv[:T].double().cpu(), None)
+    check(gx[:T], *want_x, "grad_x")
+    check(gw, *want_w, "grad_weight")
