@@ -412,3 +412,56 @@ def test_norm_of_rows_whose_squares_leave_fp32(T, H, eps):
     want_x, want_w = plain.norm_grad(gy.double(), x.double(), w.double(), inv[:T].double().cpu(), None)
     check(gx[:T], *want_x, "grad_x")
     check(gw, *want_w, "grad_weight")
+
+
+def wide_rows(T, H, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(T, H, generator=gen, device="cuda").bfloat16()
+
+
+def check_here(got, want, bound, what):
+    off = (got.double() - want).abs()
+    assert (off <= bound).all(), (what, float((off - bound).max()))
+
+
+# Launches end at 1024 blocks forward and 512 back: past twice as many rows a group of 1024
+# threads takes a third one, which uses the first one's places in LDS again.
+@pytest.mark.parametrize("T,H", [(2100, 8200), (2051, 16384), (2100, 16392), (2060, 32776),
+                                 (2049, 65536)])
+def test_norm_of_several_wide_rows_a_block(T, H):
+    x, res, w = wide_rows(T, H, 1), wide_rows(T, H, 2), norm_weight(H, T).cuda()
+    total, y = torch.empty_like(x), torch.empty_like(x)
+    inv = torch.empty(T, device="cuda")
+    codes = H % 128 == 0
+    c = torch.empty(T, H, dtype=torch.uint8, device="cuda") if codes else None
+    s = torch.empty(T, H // 128, device="cuda") if codes else None
+    api.moe_rms_norm(x, res, w, EPS, total, y, c, s, inv)
+    assert torch.equal(total, (x.float() + res.float()).bfloat16())
+    v, dv, r, dr = plain.norm(total.double(), w.double(), EPS)
+    check_here(y, v, plain.rounded16(v, dv), "y")
+    check_here(inv, r, dr, "1 / rms")
+    if codes:
+        at = [0, 1, 1023, 1024, 1025, 2047, 2048, T - 1]
+        check_codes(c[at], s[at], v[at].cpu(), dv[at].cpu())
+    # the residual stream in place, and the rows over the input's
+    api.moe_rms_norm(x, res, w, EPS, res, x)
+    assert torch.equal(res, total) and torch.equal(x, y)
+
+
+@pytest.mark.parametrize("T,H", [(1100, 8200), (1030, 16384), (1100, 16392), (1030, 32776),
+                                 (1025, 65536)])
+def test_norm_gradient_of_several_wide_rows_a_block(T, H):
+    t, gy, carried = wide_rows(T, H, 3), wide_rows(T, H, 4), wide_rows(T, H, 5)
+    w = norm_weight(H, T).cuda()
+    r = (t.double().square().mean(1) + EPS).rsqrt().float()
+    gx, gw = torch.empty_like(t), torch.empty(H, device="cuda")
+    api.moe_rms_norm_backward(gy, t, w, r, carried, gx, gw)
+    want_x, want_w = plain.norm_grad(gy.double(), t.double(), w.double(), r.double(), carried.double())
+    check_here(gx, *want_x, "grad_x")
+    check_here(gw, *want_w, "grad_weight")
+    again = torch.empty_like(gw)
+    api.moe_rms_norm_backward(gy, t, w, r, carried, carried, again)
+    assert torch.equal(carried, gx) and torch.equal(again, gw)
+    api.moe_rms_norm_backward(gy, t, w, r, None, gx, None)
+    api.moe_rms_norm_backward(gy, t, w, r, None, gy, again)
+    assert torch.equal(gy, gx) and torch.equal(again, gw)
