@@ -311,3 +311,17 @@ def test_rows_past_2_31_elements():
     # the other rows are zeros and add nothing to the sums
     for got, (want, bound), n in zip((gx[at], gu, gd), grads, ("grad_x", "grad_up", "grad_down")):
         assert ((got.double().cpu() - want).abs() <= bound).all(), n
+
+
+@pytest.mark.parametrize("T,H,I,E,k,N,C", [(1, 256, 128, 4, 2, 1, 0), (70, 384, 256, 6, 2, 2, 140),
+                                           (300, 512, 384, 4, 3, 1, 0)])
+def test_gradient_of_the_routed_weights(T, H, I, E, k, N, C):
+    """<g, y> of the layer's own gradient and expert rows, as near as its fp32 sum."""
+    layer = Layer(T, H, I, E, k, N, C, seed=T)
+    layer.forward()
+    layer.backward()
+    g, y = layer.gtotal2.double().cpu(), layer.ey.double().cpu()
+    terms = g[:, None] * y[layer.lay.token_row.cpu().long().view(T, k)]
+    want, bound = terms.sum(2), (H + 8) * ref.U32 * terms.abs().sum(2)
+    assert ((layer.gw.double().cpu() - want).abs() <= bound).all()
+    assert want.norm() > 100 * bound.norm()   # zeros, or another sign, would not do
