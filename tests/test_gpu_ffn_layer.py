@@ -325,3 +325,43 @@ def test_gradient_of_the_routed_weights(T, H, I, E, k, N, C):
     want, bound = terms.sum(2), (H + 8) * ref.U32 * terms.abs().sum(2)
     assert ((layer.gw.double().cpu() - want).abs() <= bound).all()
     assert want.norm() > 100 * bound.norm()   # zeros, or another sign, would not do
+
+
+def test_two_graphs_at_once():
+    """Two layers captured with buffers and workspaces of their own, replayed on two
+    streams at the same time with eager work in between."""
+    def make(i):
+        return Layer(150 + 60 * i, 256, 128, 4, 2, 1, 0, seed=40 + i)
+
+    alone = [make(i) for i in range(2)]
+    layers, streams = [make(i) for i in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for layer, s in zip(layers, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            layer.forward()
+            layer.backward()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            layer.forward()
+            layer.backward()
+    for i in range(4):
+        for a, b in zip(layers, alone):
+            x = torch.randn(a.x.shape, generator=torch.Generator().manual_seed(i)).bfloat16()
+            for one in (a, b):
+                one.x.copy_(x)
+            for ws in (a.ws, a.dws_s, a.bws, a.bws_s, a.nws):
+                if ws is not None:
+                    ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for graph, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for n, (a, b) in enumerate(zip(layers, alone)):
+            b.forward()
+            b.backward()
+            for (name, got), want in zip(a.results().items(), b.results().values()):
+                assert torch.equal(got, want), (i, n, name)
