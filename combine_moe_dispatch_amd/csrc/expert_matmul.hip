@@ -484,12 +484,8 @@ using Large = Config<2, 2, 8, 8>;
 using Mid = Config<2, 2, 4, 4>;
 // 64 x 16 by four waves that share the steps.
 using Few = StreamProduct<4, 1, 4, 3>;
-// fp8 where there are few large tiles and more than 128 rows an expert: 256 token rows
-// by 128 weight rows in three steps of LDS, unless 128 x 128 tiles find a compute unit
-// each (4096 x 7168, one expert: 200 rows 52 us against 35, 1021 rows 55 against 41,
-// 1500 rows 59 against 68; 8 experts of 130 rows 56 against 80).  With up to 128 rows
-// there are as many of these, two to a unit (32 experts of 8 rows 159 us against 157;
-// 16 rows and 2048 x 7168, 24.5 us against 22).
+// fp8 where there are few large tiles: 256 token rows by 128 weight rows in three steps
+// of LDS.
 using FewCodes = Config<2, 4, 4, 4>;
 
 // Large tiles from 112 rows an expert on, where some experts begin to need two
@@ -525,6 +521,22 @@ bool large_weight_tiles(const Segments& s, int K, int P) {
   const int64_t tiles = (int64_t)s.E * ((K + Large::kBu - 1) / Large::kBu) *
                         ((P + Large::kBv - 1) / Large::kBv);
   return s.pairs / s.E > 64 && tiles >= kUnits * 3 / 4;
+}
+
+// fp8 on 128 x 128 tiles in place of FewCodes': up to 128 rows an expert, where there
+// are as many of them, two to a unit (32 experts of 8 rows 159 us against 157; 16 rows
+// and 2048 x 7168, 24.5 us against 22), and while they find a compute unit each (4096 x
+// 7168, one expert: 200 rows 52 us against 35, 1021 rows 55 against 41, 1500 rows 59
+// against 68; 8 experts of 130 rows 56 against 80).  Among several experts chance gives
+// some more rows than the mean, and a second tile each (8 experts at random, 104 rows
+// 41 us against 48, 112 rows 51 against 64, 128 rows 49 against 69): a quarter more is
+// counted.
+bool narrow_codes(const Segments& s, int u) {
+  const int64_t mean = s.pairs / s.E, rows = s.E > 1 ? mean + mean / 4 : mean;
+  const int64_t busy = s.E < s.pairs ? s.E : s.pairs;
+  const int64_t tiles = (rows + NarrowCodes::kBv - 1) / NarrowCodes::kBv *
+                        ((u + NarrowCodes::kBu - 1) / NarrowCodes::kBu);
+  return rows <= NarrowCodes::kBv || busy * tiles <= kUnits;
 }
 
 template <class C, int ACT>
@@ -573,9 +585,7 @@ template <int ACT>
 hipError_t launch_forward(const MatmulParams& p, bool fp8, hipStream_t st) {
   if (fp8) {
     if (large_codes(p.seg, p.P)) return launch_codes<Codes, 2, ACT>(p, st);
-    if (p.seg.pairs / p.seg.E <= 128 ||
-        tiles_of(p.seg, p.P, NarrowCodes::kBu, NarrowCodes::kBv) <= kUnits)
-      return launch_codes<NarrowCodes, 2, ACT>(p, st);
+    if (narrow_codes(p.seg, p.P)) return launch_codes<NarrowCodes, 2, ACT>(p, st);
     return launch_codes<FewCodes, 3, ACT>(p, st);
   }
   if (large_tiles(p.seg, p.P)) return launch_tiles<Large, ACT>(p, st);
