@@ -360,15 +360,18 @@ int groups_of(int T, int H) {
   return blocks_of(T, s, kGradBlocks) * (s.threads < 256 ? 256 / s.threads : 1);
 }
 
-// call(L, V) as constants
+// call(L, V) as constants, those of split_of
 template <class Call>
 void with_split(Split s, const Call& call) {
   const auto vectors = [&](auto l) {
     using std::integral_constant;
-    if (s.vectors == 1) call(l, integral_constant<int, 1>{});
-    else if (s.vectors == 2) call(l, integral_constant<int, 2>{});
-    else if (s.vectors == 4) call(l, integral_constant<int, 4>{});
-    else if constexpr (decltype(l)::value == 1024) call(l, integral_constant<int, 8>{});
+    constexpr int kL = decltype(l)::value, kMost = kL < 64 ? 1 : kL < 256 ? 2 : kL < 1024 ? 4 : 8;
+    if (s.vectors == 1) return call(l, integral_constant<int, 1>{});
+    if constexpr (kMost >= 2)
+      if (s.vectors == 2) return call(l, integral_constant<int, 2>{});
+    if constexpr (kMost >= 4)
+      if (s.vectors == 4) return call(l, integral_constant<int, 4>{});
+    if constexpr (kMost >= 8) call(l, integral_constant<int, 8>{});
   };
   switch (s.threads) {
     case 16: vectors(std::integral_constant<int, 16>{}); break;

@@ -23,6 +23,16 @@ def test_built_library(tmp_path):
     assert products > 1000 and loads > 1000   # the listing was read
 
 
+@pytest.mark.skipif(not os.path.exists(LIB), reason="libmoe_dispatch.so not built")
+@pytest.mark.parametrize("kernel", [b"rms_norm_kernel", b"rms_norm_grad_kernel"])
+def test_norms_are_built_for_what_is_launched(kernel):
+    """Threads to a row and vectors a thread: the pairs that a call can reach, no others."""
+    names = re.findall(b"%d%sILi(\\d+)ELi(\\d+)E" % (len(kernel), kernel), open(LIB, "rb").read())
+    assert {(int(a), int(b)) for a, b in names} == {
+        (16, 1), (32, 1), (64, 1), (64, 2), (256, 1), (256, 2), (256, 4),
+        (1024, 1), (1024, 2), (1024, 4), (1024, 8)}
+
+
 def listing(*lines):
     """lines: text, or (text, index of the line it branches to)."""
     out = ["0000000000001000 <kernel>:"]
