@@ -80,9 +80,10 @@ __device__ __forceinline__ void add8(float (&v)[8], const float* p) {
 
 __device__ __forceinline__ float sigmoid_f32(float v) { return 1.0f / (1.0f + expf(-v)); }
 
-// The same for results that are rounded to bf16 next: the hardware's 2^x and
-// reciprocal, off by (1 + |v|) 2^-23 of the value or so where the rounding is
-// off by 2^-8.  A tile's activations are thousands of these per lane.
+// The same for results that are rounded to bf16 or to 8 bits next, slopes among
+// them: the hardware's 2^x and reciprocal, off by (1 + |v|) 2^-23 of the value or so
+// where the rounding is off by 2^-8 or more.  A tile's activations are thousands of
+// these per lane.
 __device__ __forceinline__ float sigmoid_short(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
 }

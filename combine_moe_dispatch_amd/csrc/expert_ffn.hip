@@ -119,8 +119,10 @@ template <class C>
 constexpr int kUpLds = Fp8Product<C, kStages<C>>::kLds + C::kWu * C::kBv * 4;
 
 // 4096 tokens, top-8 of 32 experts of 7168 x 2048: 884 us, 2.2 PFLOP/s (a large
-// product with one scale 3.1); the matrix units are 48 % busy, beside 6.4 vector
-// operations a product; first loads, activation and stores take 163 us of it.  128
+// product with one scale 3.1); the matrix units are 48 % busy.  The sums are scaled by
+// vector instructions and so fill the vector registers: eight waves of 128 x 64, which
+// read 192 KB out of LDS a step and bring 64 KB in, 2048 cycles at 128 bytes a cycle and
+// as many as their products take.  First loads, activation and stores take 163 us.  128
 // tokens: the weights' way from memory, 5.5 TB/s in 168 us.
 template <class C>
 __global__ void __launch_bounds__(C::kThreads)
@@ -279,8 +281,9 @@ ffn_join_down_kernel(Segments seg, const float* parts, int shares, const uint16_
 // Backward
 // ---------------------------------------------------------------------------
 // Placed rows of grad_y to 8 bits and of x to bf16 (code times scale, half a bf16
-// step off; NULL: not wanted): a stream, 4 rows a block (16384 rows of 7168: 705 MB
-// in 158 us, 4.5 TB/s).
+// step off: a token's scale cannot be taken out of a sum over tokens, and what the
+// rounding leaves would be a second product; NULL: not wanted): a stream, 4 rows a block
+// (16384 rows of 7168: 705 MB in 158 us, 4.5 TB/s).
 constexpr int kPrepareRows = 4, kPrepareThreads = 256;
 
 struct PrepareParams {
@@ -587,7 +590,10 @@ int64_t even_tiles(int pairs, int E, int u, int cols) {
 // by call: one token 46 against 26 us, 64 tokens 54 against 32, 512 tokens 76 against
 // 46; twice the blocks 31, 41 and 69), and with a few rows an expert such tiles read
 // the weights faster than the larger ones (one token of 8 of 32 experts, up projections
-// 53 us against 41 + 5).  There is no second reason for one share of a down projection,
+// 53 us against 41 + 5).  Up to 4 rows an expert that is one share of more tiles than
+// units, about as fast as whole tiles (the block of 7168 x 2048, top-8 of 32 experts: 4
+// tokens 171 us against 182, 16 tokens 242 against 239; of 256: 16 tokens 726 against 740,
+// 128 tokens 1.82 ms against 1.79).  There is no second reason for one share of a down projection,
 // whose tiles are as small, nor of the up projections where tiles of 256 x 64 are as
 // many (1021 tokens of one expert 74 us against 69, 600 tokens 63 against 60; but one
 // token of 8 experts, which makes half as many, 68 against 80).

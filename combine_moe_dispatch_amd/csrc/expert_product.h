@@ -761,7 +761,10 @@ inline int64_t tiles_of(const Segments& s, int u, int bu, int bv) {
 // product than smaller tiles (32 experts of 4096 x 7168 against 128 x 256 tiles: 16
 // rows each 161 us against 164, 64 rows 169 against 187, 128 rows 196 against 234, 512
 // rows 499 against 624; one expert and 2048 rows, which make 128 tiles, with the way
-// back to 7168 columns 137 against 117).
+// back to 7168 columns 137 against 117).  Uneven routing gains more (rows by 1 / rank over
+// the 32 experts: 16 rows 174 against 196, 64 rows 280 against 395) unless few experts have
+// them all and the tiles are few after all (16 rows in one expert 82 against 71, 40 rows in
+// eight 69 against 55).
 using Codes = Config<2, 4, 8, 4>;
 // 128 x 128, two blocks to a compute unit.
 using NarrowCodes = Config<2, 4, 4, 2>;
