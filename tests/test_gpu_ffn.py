@@ -404,3 +404,23 @@ def test_refusals_on_tensors():
         api.moe_expert_ffn(*args, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(api.MoeError):                     # a bf16 payload
         api.moe_expert_ffn(api.Shape(8, 128, 2, 1, 1, 0, 0), *args[1:])
+
+
+@pytest.mark.parametrize("T,E,k,N,C,H,I,dense", [
+    (2, 1, 1, 1, 0, 2048, 2048, True),      # both projections in shares
+    (60, 4, 2, 2, 100, 256, 2048, False),   # the second alone, fixed capacity
+    (260, 3, 2, 1, 0, 256, 384, False),     # neither
+    (2100, 1, 1, 1, 0, 128, 4096, True),    # large tiles
+])
+def test_residual_in_place(T, E, k, N, C, H, I, dense):
+    case = Case(T, E, k, N, C, H, I, seed=T, dense=dense)
+    r = case.bf16(H).cuda()
+    y, _ = case.forward(r)
+    before = r.clone()
+    api.moe_expert_ffn(case.shape, case.ffn, case.x, case.xs, case.lay, case.up, case.us, case.down,
+                       case.ds, r, r, None, case.poisoned(False))
+    placed = torch.zeros(case.rows, dtype=torch.bool, device="cuda")
+    for a, b in case.spans:
+        placed[a:b] = True
+    assert torch.equal(r[placed], y[:case.rows][placed])
+    assert torch.equal(r[~placed], before[~placed])

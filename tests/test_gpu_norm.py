@@ -465,3 +465,13 @@ def test_norm_gradient_of_several_wide_rows_a_block(T, H):
     api.moe_rms_norm_backward(gy, t, w, r, None, gx, None)
     api.moe_rms_norm_backward(gy, t, w, r, None, gy, again)
     assert torch.equal(gy, gx) and torch.equal(again, gw)
+
+
+@pytest.mark.parametrize("T,H", [(3000, 512), (1100, 8192), (1030, 16384), (3, 40960)])
+def test_norm_in_place_the_other_way(T, H):
+    """total over the input and y over the residual."""
+    x, res, w = wide_rows(T, H, 7), wide_rows(T, H, 8), norm_weight(H, 7).cuda()
+    t, y = torch.empty_like(x), torch.empty_like(x)
+    api.moe_rms_norm(x, res, w, EPS, t, y)
+    api.moe_rms_norm(x, res, w, EPS, x, res)
+    assert torch.equal(x, t) and torch.equal(res, y)
