@@ -2,6 +2,9 @@
 shared expert, combine, the next layer's norm, and back through all of it; against
 fp64 without any rounding; in one HIP graph; on given streams at once; and sizes past
 32 bits."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -365,3 +368,53 @@ def test_two_graphs_at_once():
             b.backward()
             for (name, got), want in zip(a.results().items(), b.results().values()):
                 assert torch.equal(got, want), (i, n, name)
+
+
+FIRST = """
+import sys, torch
+sys.path.insert(0, ".")
+from combine_moe_dispatch_amd import api
+T, H, I = {T}, {H}, {I}
+u8 = lambda *s: torch.randint(0, 100, s, dtype=torch.uint8, device="cuda")
+f32 = lambda *s: torch.rand(*s, device="cuda") * 1e-3
+bf = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+x, xs, w = u8(T, H), f32(T, H // 128), (u8(1, 2 * I, H), f32(1, 2 * I // 128, H // 128),
+                                        u8(1, H, I), f32(1, H // 128, I // 128))
+up, codes, scales = bf(1, 2 * I, H), u8(1, 2 * I, H), f32(1, 2 * I // 128, H // 128)
+t, nw, y, pre, gy = bf(T, H), 1 + f32(H), bf(T, H), bf(T, 2 * I), bf(T, H)
+gx, gu, gd, n, inv, gn, gw = bf(T, H), bf(1, 2 * I, H), bf(1, H, I), bf(T, H), f32(T), bf(T, H), f32(H)
+s, f = api.Shape(T, H, 1, 1, 1, 0, 1), api.Ffn(H, I)
+ws, bws = (api.alloc_ffn_workspace(s, f, "cuda", b) for b in (False, True))
+nws = api.alloc_rms_norm_workspace(T, H, "cuda")
+outs = (codes, scales, y, pre, gx, gu, gd, n, inv, gn, gw)
+torch.cuda.synchronize()
+def step():
+    api.moe_quantize_weight(up, codes, scales)
+    api.moe_expert_ffn(s, f, x, xs, None, *w, None, y, pre, ws)
+    api.moe_expert_ffn_backward(s, f, gy, x, xs, None, *w, pre, gx, gu, gd, bws)
+    api.moe_rms_norm(t, None, nw, 1e-6, None, n, None, None, inv)
+    api.moe_rms_norm_backward(gy, t, nw, inv, None, gn, gw, nws)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+for _ in range(3):
+    for o in outs:
+        o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    got = [o.clone() for o in outs]
+    step()
+    torch.cuda.synchronize()
+    for a, b in zip(got, outs):
+        assert torch.equal(a, b) and a.any()
+print("captured ok")
+"""
+
+
+@pytest.mark.parametrize("T,H,I", [(3, 2048, 2048), (300, 256, 384), (1500, 128, 11136)])
+def test_first_calls_inside_a_capture(T, H, I):
+    """A process whose first calls of these kernels are captured ones: in shares, and on
+    smaller and larger tiles."""
+    r = subprocess.run([sys.executable, "-c", FIRST.format(T=T, H=H, I=I)], capture_output=True,
+                       text=True, timeout=100)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stderr[-2000:]
